@@ -410,20 +410,28 @@ def _types():
     return _x_types, _fp8_types
 
 
-def _raw_stream(stream, index):
-    """The address of ``stream``, or of the current stream of GPU ``index``."""
-    if stream is not None:
-        return int(stream)
+def _on(stream, index):
+    """(address, side) of the stream that a call on GPU ``index`` runs on: the current one, or ``stream``; side is the latter
+    as a torch stream where it is not the current one, else None."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(index)
+    here = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None or int(stream) == here:
+        return here, None
+    return int(stream), torch.cuda.ExternalStream(int(stream), device=index)
 
 
-def _hold(t, stream):
-    """A buffer made here for a call on a stream other than the current one must not be handed out again
-    before that stream is done with it."""
-    if stream is not None:
-        import torch
-        t.record_stream(torch.cuda.ExternalStream(int(stream), device=t.device))
+def _buffer(shape, dtype, device, side, output=True):
+    """A new buffer for a call that runs on ``side`` (None: the current stream), from that stream's pool: the current
+    one's hands out blocks that kernels waiting there still use. An output is recorded on the current stream, where the
+    caller may use and drop it."""
+    import torch
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(here)
     return t
 
 
@@ -461,22 +469,19 @@ def quantize_fp8(x, fmt=None, rows=1, transposed=False, stream=None):
         raise ValueError("the rows of x must be contiguous")
     rg, cg = (R + 127) // 128, (C + 127) // 128
     dev = x.device
-    codes = torch.empty((R, cg * 128), dtype=fmt, device=dev)
-    scale = torch.empty((cg, R) if rows == 1 else (rg, cg), dtype=torch.float32, device=dev)
+    address, side = _on(stream, x.get_device())
+    codes = _buffer((R, cg * 128), fmt, dev, side)
+    scale = _buffer((cg, R) if rows == 1 else (rg, cg), torch.float32, dev, side)
     codes_t = scale_t = None
     if transposed:
-        codes_t = torch.empty((C, rg * 128), dtype=fmt, device=dev)
-        scale_t = torch.empty((rg, C) if rows == 1 else (cg, rg), dtype=torch.float32, device=dev)
+        codes_t = _buffer((C, rg * 128), fmt, dev, side)
+        scale_t = _buffer((rg, C) if rows == 1 else (cg, rg), torch.float32, dev, side)
     if R and C:
         st = lib().tbl_quantize_fp8(x.data_ptr(), R, C, ld, xt, ft, rows, codes.data_ptr(), cg * 128, scale.data_ptr(),
                                     codes_t.data_ptr() if transposed else None, rg * 128,
-                                    scale_t.data_ptr() if transposed else None, _raw_stream(stream, x.get_device()))
+                                    scale_t.data_ptr() if transposed else None, address)
         if st:
             _check(st, "tbl_quantize_fp8")
-    if stream is not None:
-        for t in (codes, scale, codes_t, scale_t):
-            if t is not None:
-                _hold(t, stream)
     q = Fp8Blocks(codes if C == cg * 128 else codes[:, :C], scale, rows)
     if not transposed:
         return q
@@ -503,7 +508,7 @@ def _refuse_fp8_operand(q, name, device):
     raise ValueError(f"{name} must be a GPU tensor on {device} (got codes on {t.device}, scale on {s.device})")
 
 
-def _fp8_operand(q, name, device, index, stream):
+def _fp8_operand(q, name, device, index, side):
     """(codes, row stride in bytes, format) of a GEMM operand on GPU ``index``; codes whose rows do not start on 16-byte
     boundaries are copied to a buffer where they do."""
     t, s, rows = q.codes, q.scale, q.rows
@@ -523,9 +528,8 @@ def _fp8_operand(q, name, device, index, stream):
     if K > 1 and step != 1 or ld < K or ld % 16 or t.data_ptr() % 16:
         import torch
         ld = (K + 127) // 128 * 128
-        on = torch.cuda.current_stream(device) if stream is None else torch.cuda.ExternalStream(int(stream), device=device)
-        with torch.cuda.stream(on):
-            wide = torch.empty((R, ld), dtype=torch.uint8, device=device)
+        wide = _buffer((R, ld), torch.uint8, device, side, output=False)
+        with torch.cuda.stream(side):   # None: the current one
             wide[:, :K].copy_(t.view(torch.uint8))
         t = wide
     return t, ld, fmt
@@ -546,8 +550,9 @@ def gemm_fp8(a, b, add=None, out=None, out_dtype=None, workspace=None, stream=No
     import torch
     x_types = _x_types or _types()[0]
     device, index = a.codes.device, a.codes.get_device()
-    at, lda, fa = _fp8_operand(a, "A", device, index, stream)
-    bt, ldb, fb = _fp8_operand(b, "B", device, index, stream)
+    address, side = _on(stream, index) if index >= 0 else (0, None)
+    at, lda, fa = _fp8_operand(a, "A", device, index, side)
+    bt, ldb, fb = _fp8_operand(b, "B", device, index, side)
     M, K = a.codes.shape
     N = b.codes.shape[0]
     if b.codes.shape[1] != K:
@@ -558,9 +563,7 @@ def gemm_fp8(a, b, add=None, out=None, out_dtype=None, workspace=None, stream=No
     if ot is None:
         raise TypeError(f"unsupported output dtype {out_dtype}")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=device)
-        if stream is not None:
-            _hold(out, stream)
+        out = _buffer((M, N), out_dtype, device, side)
     elif out.shape != (M, N) or out.dtype != out_dtype or not out.is_contiguous() or out.get_device() != index:
         raise ValueError("out must be a contiguous (M, N) tensor of the output dtype on A's device")
     if add is not None and (add.shape != (M, N) or add.dtype != torch.float32 or not add.is_contiguous()
@@ -568,13 +571,12 @@ def gemm_fp8(a, b, add=None, out=None, out_dtype=None, workspace=None, stream=No
         raise ValueError("add must be a contiguous float32 (M, N) tensor on A's device")
     need = _gemm_fp8_bytes(M, N, K)
     if need > 0 and workspace is None:
-        workspace = _hold(torch.empty(need, dtype=torch.uint8, device=device), stream)
+        workspace = _buffer(need, torch.uint8, device, side, output=False)
     if workspace is not None:
         _device_tensor(workspace, "workspace", torch.uint8, need, device)
     st = lib().tbl_gemm_fp8(at.data_ptr(), lda, fa, a.scale.data_ptr(), a.rows, bt.data_ptr(), ldb, fb, b.scale.data_ptr(),
                             b.rows, None if add is None else add.data_ptr(), out.data_ptr(), ot, M, N, K,
-                            None if need <= 0 else workspace.data_ptr(), 0 if need <= 0 else workspace.numel(),
-                            _raw_stream(stream, index))
+                            None if need <= 0 else workspace.data_ptr(), 0 if need <= 0 else workspace.numel(), address)
     if st:
         _check(st, "tbl_gemm_fp8")
     return out
@@ -615,19 +617,18 @@ def newton_schulz(x, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
         raise ValueError("the rows of x must be contiguous")
     a, b, c = (float(v) for v in coefficients)
     device = x.device
+    address, side = _on(stream, x.get_device())
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=device)
-        if stream is not None:
-            _hold(out, stream)
+        out = _buffer(x.shape, out_dtype, device, side)
     elif out.shape != x.shape or out.dtype != out_dtype or not out.is_contiguous() or out.device != device:
         raise ValueError("out must be a contiguous tensor of x's shape and the output dtype on x's device")
     need = newton_schulz_workspace(batch, R, C)
     if workspace is None:
-        workspace = _hold(torch.empty(need, dtype=torch.uint8, device=device), stream)
+        workspace = _buffer(need, torch.uint8, device, side, output=False)
     _device_tensor(workspace, "workspace", torch.uint8, need, device)
     st = lib().tbl_newton_schulz(x.data_ptr(), batch, R, C, ld, x.stride(0) if batch > 1 else 0, x_types[x.dtype],
                                  out.data_ptr(), x_types[out_dtype], int(steps), a, b, c, float(eps), workspace.data_ptr(),
-                                 workspace.numel(), _raw_stream(stream, x.get_device()))
+                                 workspace.numel(), address)
     _check(st, "tbl_newton_schulz")
     return out
 
