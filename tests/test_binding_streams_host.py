@@ -78,6 +78,7 @@ def gpu(monkeypatch):
         monkeypatch.setattr(torch, name, maker(getattr(torch, name)))
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(current[-1]))
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: current[-1], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
@@ -103,6 +104,25 @@ def fp8_calls():
     }
 
 
+def other_calls():
+    a, b = fake((512, 512), torch.float16), fake((512, 512), torch.float16)
+    i = fake((64, 128), torch.int32)
+    return {
+        "gemm": lambda s: tbl.gemm(a, b, stream=s),
+        "gemm of a tile": lambda s: tbl.gemm(a, b, tile=(256, 256, 32), stream=s),
+        "gemm_dynamic": lambda s: tbl.gemm_dynamic(a, b, num_programs=3, stream=s),
+        "gemm_dynamic_noalloc": lambda s: tbl.gemm_dynamic_noalloc(a, b, num_programs=3, stream=s),
+        "gemm_lds_layout": lambda s: tbl.gemm_lds_layout(a, b, tbl.LDS_LAYOUTS[0], stream=s),
+        "mfma_rate": lambda s: tbl.mfma_rate(a, b, workgroups=4, stream=s)[1:],
+        "tile_map": lambda s: tbl.tile_map(tbl.ROW, 4, 4, stream=s)[:2],
+        "transpose_i32": lambda s: tbl.transpose_i32(i, stream=s),
+        "copy16": lambda s: tbl.copy16(i, stream=s),
+    }
+
+
+CALLS = {**fp8_calls(), **other_calls()}
+
+
 def outputs(result):
     if isinstance(result, tbl.Fp8Blocks):
         return [result.codes, result.scale]
@@ -111,10 +131,10 @@ def outputs(result):
     return [result] if isinstance(result, torch.Tensor) else []
 
 
-@pytest.mark.parametrize("name", list(fp8_calls()))
+@pytest.mark.parametrize("name", list(CALLS))
 def test_buffers_come_from_the_stream_of_the_call(gpu, name):
     calls, made = gpu
-    result = fp8_calls()[name](SIDE)
+    result = CALLS[name](SIDE)
     assert made and set(made.values()) == {SIDE}
     (_, args), = calls.calls
     assert args[-1] == SIDE
@@ -123,10 +143,10 @@ def test_buffers_come_from_the_stream_of_the_call(gpu, name):
 
 
 @pytest.mark.parametrize("stream", [None, CURRENT])
-@pytest.mark.parametrize("name", list(fp8_calls()))
+@pytest.mark.parametrize("name", list(CALLS))
 def test_buffers_of_a_call_on_the_current_stream(gpu, name, stream):
     calls, made = gpu
-    fp8_calls()[name](stream)
+    CALLS[name](stream)
     assert made and set(made.values()) == {CURRENT} and Gpu.recorded == []
     (_, args), = calls.calls
     assert args[-1] == CURRENT

@@ -161,11 +161,29 @@ def _check(status, where, allow_warning=False):
     return status
 
 
-def _stream(stream):
-    if stream is not None:
-        return ctypes.c_void_p(int(stream))
+def _on(stream, index):
+    """(address, side) of the stream that a call on GPU ``index`` runs on: the current one, or ``stream``; side is the latter
+    as a torch stream where it is not the current one, else None."""
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    here = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None or int(stream) == here:
+        return here, None
+    return int(stream), torch.cuda.ExternalStream(int(stream), device=index)
+
+
+def _buffer(shape, dtype, device, side, output=True):
+    """A new buffer for a call that runs on ``side`` (None: the current stream), from that stream's pool: the current
+    one's hands out blocks that kernels waiting there still use. An output is recorded on the current stream, where the
+    caller may use and drop it."""
+    import torch
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(here)
+    return t
 
 
 def _ptr(t):
@@ -216,16 +234,17 @@ def gemm(a, b, c=None, mode=ROW, group=1, persistent=False, num_programs=0, out_
     N = b.shape[1]
     out_dtype = out_dtype or (c.dtype if c is not None else a.dtype)
     dt = _gemm_dtype(a, out_dtype)
+    _device_tensor(a, "A")
+    s, side = _on(stream, a.get_device())
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        c = _buffer((M, N), out_dtype, a.device, side)
     if c.shape != (M, N) or not c.is_contiguous() or c.dtype != out_dtype:
         raise ValueError("C must be a contiguous (M, N) tensor of the output dtype")
-    for t, name in ((a, "A"), (b, "B"), (c, "C")):
+    for t, name in ((b, "B"), (c, "C")):
         _device_tensor(t, name, device=a.device)
     if trace is not None:
         bm, bn, _ = tile if tile is not None else gemm_tile_shape(M, N, K)
         _device_tensor(trace, "trace", torch.int32, 8 * (-(-M // bm)) * (-(-N // bn)), a.device)
-    s = _stream(stream)
     if tile is None and trace is None:
         st = lib().tbl_gemm(_ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode), int(group),
                             int(bool(persistent)), int(num_programs), s)
@@ -258,8 +277,8 @@ def dynamic_workspace(num_programs, device="cuda"):
     return torch.zeros(dynamic_workspace_ints(num_programs), dtype=torch.int32, device=device)
 
 
-def _dynamic_args(a, b, c, out_dtype, trace):
-    """Shared checks of the dynamic-schedule calls: returns (M, N, K, dtype code, c, T)."""
+def _dynamic_args(a, b, c, out_dtype, trace, stream):
+    """Shared checks of the dynamic-schedule calls: returns (M, N, K, dtype code, c, T, stream's address, side)."""
     import torch
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[0]:
         raise ValueError(f"shape mismatch {tuple(a.shape)} x {tuple(b.shape)}")
@@ -271,16 +290,18 @@ def _dynamic_args(a, b, c, out_dtype, trace):
     N = b.shape[1]
     out_dtype = out_dtype or (c.dtype if c is not None else a.dtype)
     dt = _gemm_dtype(a, out_dtype)
+    _device_tensor(a, "A")
+    s, side = _on(stream, a.get_device())
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        c = _buffer((M, N), out_dtype, a.device, side)
     if c.shape != (M, N) or not c.is_contiguous() or c.dtype != out_dtype:
         raise ValueError("C must be a contiguous (M, N) tensor of the output dtype")
-    for t, name in ((a, "A"), (b, "B"), (c, "C")):
+    for t, name in ((b, "B"), (c, "C")):
         _device_tensor(t, name, device=a.device)
     T = (-(-M // 256)) * (-(-N // 256))
     if trace is not None:
         _device_tensor(trace, "trace", torch.int32, 8 * T, a.device)
-    return M, N, K, dt, c, T
+    return M, N, K, dt, c, T, s, side
 
 
 def gemm_dynamic_noalloc(a, b, c=None, mode=ROW, group=1, num_programs=0, out_dtype=None, trace=None,
@@ -289,9 +310,9 @@ def gemm_dynamic_noalloc(a, b, c=None, mode=ROW, group=1, num_programs=0, out_dt
     a device array of the library (one per GPU, for at most NOALLOC_MAX_PROGRAMS workgroups), so the
     library call allocates nothing (``c`` is allocated here when not given). Calls that overlap in
     time on one GPU share that array and must be serialised. Returns c."""
-    M, N, K, dt, c, _ = _dynamic_args(a, b, c, out_dtype, trace)
+    M, N, K, dt, c, _, s, _ = _dynamic_args(a, b, c, out_dtype, trace, stream)
     st = lib().tbl_gemm_dynamic_noalloc(_ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode), int(group),
-                                        int(num_programs), _ptr(trace), _stream(stream))
+                                        int(num_programs), _ptr(trace), s)
     _check(st, "tbl_gemm_dynamic_noalloc")
     return c
 
@@ -304,14 +325,14 @@ def gemm_dynamic(a, b, c=None, mode=ROW, group=1, num_programs=0, workspace=None
     min(T, 4 x CUs)). ``trace``: int32 CUDA tensor of 8*T entries, indexed by order position.
     Returns c."""
     import torch
-    M, N, K, dt, c, T = _dynamic_args(a, b, c, out_dtype, trace)
+    M, N, K, dt, c, T, s, side = _dynamic_args(a, b, c, out_dtype, trace, stream)
     if workspace is None:
         P = int(num_programs) or max(1, min(T, 4 * device_info()["num_cus"]))
-        workspace = dynamic_workspace(P, a.device)
+        with torch.cuda.stream(side):   # None: the current one
+            workspace = dynamic_workspace(P, a.device)
     _device_tensor(workspace, "workspace", torch.int32, device=a.device)
     st = lib().tbl_gemm_dynamic(_ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode), int(group),
-                                int(num_programs), _ptr(workspace), workspace.numel(), _ptr(trace),
-                                _stream(stream))
+                                int(num_programs), _ptr(workspace), workspace.numel(), _ptr(trace), s)
     _check(st, "tbl_gemm_dynamic")
     return c
 
@@ -341,16 +362,18 @@ def gemm_lds_layout(a, b, layout, c=None, mode=ROW, group=1, persistent=False, n
         raise ValueError("A and B must be contiguous row-major")
     M, K = a.shape
     N = b.shape[1]
+    _device_tensor(a, "A")
+    s, side = _on(stream, a.get_device())
     if c is None:
-        c = torch.empty((M, N), dtype=torch.float16, device=a.device)
+        c = _buffer((M, N), torch.float16, a.device, side)
     if c.shape != (M, N) or not c.is_contiguous() or c.dtype != torch.float16:
         raise ValueError("C must be a contiguous (M, N) fp16 tensor")
-    for t, name in ((a, "A"), (b, "B"), (c, "C")):
+    for t, name in ((b, "B"), (c, "C")):
         _device_tensor(t, name, device=a.device)
     app, amp, bv, bpp, bmp = (int(x) for x in layout)
     fn = lib().tbl_gemm_lds_layout16 if mfma16 else lib().tbl_gemm_lds_layout
     st = fn(_ptr(a), _ptr(b), _ptr(c), M, N, K, F16, int(mode), int(group), int(bool(persistent)),
-            int(num_programs), app, amp, bv, bpp, bmp, _stream(stream))
+            int(num_programs), app, amp, bv, bpp, bmp, s)
     _check(st, "tbl_gemm_lds_layout16" if mfma16 else "tbl_gemm_lds_layout")
     return c
 
@@ -368,11 +391,14 @@ def mfma_rate(a, b, workgroups=256, iters=4000, stream=None):
     _device_tensor(a, "a")
     _device_tensor(b, "b", device=a.device)
     elems = min(a.numel(), b.numel())
-    out = torch.empty(256 * int(workgroups), dtype=torch.float32, device=a.device)
-    cycles = torch.zeros(2, dtype=torch.int64, device=a.device)
+    s, side = _on(stream, a.get_device())
+    out = _buffer(256 * int(workgroups), torch.float32, a.device, side)
+    cycles = _buffer(2, torch.int64, a.device, side)
+    with torch.cuda.stream(side):   # None: the current one
+        cycles.zero_()
     dtype = BF16 if a.dtype == torch.bfloat16 else F16
     st = lib().tbl_mfma_rate(_ptr(a), _ptr(b), elems, dtype, int(workgroups), int(iters), _ptr(out),
-                             _ptr(cycles), _stream(stream))
+                             _ptr(cycles), s)
     _check(st, "tbl_mfma_rate")
     flops = 2 * 32 * 32 * 16 * 16 * int(iters) * 4 * int(workgroups)
     return flops, out, cycles
@@ -408,31 +434,6 @@ def _types():
         _fp8_types = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
         _x_types = {torch.float16: X_F16, torch.bfloat16: X_BF16, torch.float32: X_F32}
     return _x_types, _fp8_types
-
-
-def _on(stream, index):
-    """(address, side) of the stream that a call on GPU ``index`` runs on: the current one, or ``stream``; side is the latter
-    as a torch stream where it is not the current one, else None."""
-    import torch
-    here = torch._C._cuda_getCurrentRawStream(index)
-    if stream is None or int(stream) == here:
-        return here, None
-    return int(stream), torch.cuda.ExternalStream(int(stream), device=index)
-
-
-def _buffer(shape, dtype, device, side, output=True):
-    """A new buffer for a call that runs on ``side`` (None: the current stream), from that stream's pool: the current
-    one's hands out blocks that kernels waiting there still use. An output is recorded on the current stream, where the
-    caller may use and drop it."""
-    import torch
-    if side is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(device)
-    with torch.cuda.stream(side):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if output:
-        t.record_stream(here)
-    return t
 
 
 def quantize_fp8(x, fmt=None, rows=1, transposed=False, stream=None):
@@ -648,14 +649,18 @@ def tile_map(mode, grid_m, grid_n, group=1, out_m=None, out_n=None, device="cuda
     power-of-two grids (the table is still written)."""
     import torch
     T = grid_m * grid_n
+    given = [t for t in (out_m, out_n) if t is not None]
+    device = given[0].device if given else torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"out_m and out_n must be GPU tensors (got device {device})")
+    s, side = _on(stream, torch.cuda.current_device() if device.index is None else device.index)
     if out_m is None:
-        out_m = torch.empty(T, dtype=torch.int32, device=device)
+        out_m = _buffer(T, torch.int32, device, side)
     if out_n is None:
-        out_n = torch.empty(T, dtype=torch.int32, device=device)
+        out_n = _buffer(T, torch.int32, device, side)
     _device_tensor(out_m, "out_m", torch.int32, T)
     _device_tensor(out_n, "out_n", torch.int32, T, out_m.device)
-    st = lib().tbl_tile_map(int(mode), int(grid_m), int(grid_n), int(group), _ptr(out_m), _ptr(out_n),
-                            _stream(stream))
+    st = lib().tbl_tile_map(int(mode), int(grid_m), int(grid_n), int(group), _ptr(out_m), _ptr(out_n), s)
     _check(st, "tbl_tile_map", allow_warning=True)
     return out_m, out_n, st
 
@@ -666,13 +671,14 @@ def transpose_i32(x, out=None, layout=T_XOR, stream=None):
     if x.dim() != 2 or x.dtype != torch.int32 or not x.is_contiguous():
         raise ValueError("expected a contiguous 2-D int32 tensor")
     rows, cols = x.shape
-    if out is None:
-        out = torch.empty((cols, rows), dtype=torch.int32, device=x.device)
     _device_tensor(x, "x")
+    s, side = _on(stream, x.get_device())
+    if out is None:
+        out = _buffer((cols, rows), torch.int32, x.device, side)
     if out.shape != (cols, rows):
         raise ValueError(f"out must be ({cols}, {rows})")
     _device_tensor(out, "out", torch.int32, device=x.device)
-    st = lib().tbl_transpose_i32(_ptr(x), _ptr(out), rows, cols, int(layout), _stream(stream))
+    st = lib().tbl_transpose_i32(_ptr(x), _ptr(out), rows, cols, int(layout), s)
     _check(st, "tbl_transpose_i32")
     return out
 
@@ -683,16 +689,17 @@ def copy16(src, dst=None, nontemporal=False, stream=None):
     import torch
     if not src.is_contiguous():
         raise ValueError("src must be contiguous")
+    _device_tensor(src, "src")
+    s, side = _on(stream, src.get_device())
     if dst is None:
-        dst = torch.empty_like(src)
+        dst = _buffer(src.shape, src.dtype, src.device, side)
     if not dst.is_contiguous():
         raise ValueError("dst must be contiguous")
     nbytes = src.numel() * src.element_size()
     if dst.numel() * dst.element_size() != nbytes:
         raise ValueError("src and dst must hold the same number of bytes")
-    _device_tensor(src, "src")
     _device_tensor(dst, "dst", device=src.device)
-    st = lib().tbl_copy16(_ptr(src), _ptr(dst), nbytes, 1 if nontemporal else 0, _stream(stream))
+    st = lib().tbl_copy16(_ptr(src), _ptr(dst), nbytes, 1 if nontemporal else 0, s)
     _check(st, "tbl_copy16")
     return dst
 
