@@ -16,12 +16,13 @@ CURRENT, SIDE = 0x1000, 0x2000
 
 
 class Gpu(torch.Tensor):
-    """A CPU tensor that says that it is on GPU 0."""
+    """A CPU tensor that says that it is on GPU ``at``."""
 
     is_cuda = property(lambda self: True)
+    at = 0
 
     def get_device(self):
-        return 0
+        return Gpu.at
 
     def record_stream(self, stream):
         Gpu.recorded.append((self.data_ptr(), stream.cuda_stream))
@@ -36,7 +37,7 @@ class Calls:
     """The library: sizes are the real one's, launches are noted."""
 
     def __init__(self, real):
-        self.real, self.calls = real, []
+        self.real, self.calls, self.on = real, [], []
 
     def __getattr__(self, name):
         if name.endswith("_workspace") or name in ("tbl_gemm_tile_shape", "tbl_status_string"):
@@ -46,6 +47,7 @@ class Calls:
 
         def call(*args):
             self.calls.append((name, [getattr(a, "value", a) for a in args]))
+            self.on.append(Gpu.current)
             return tbl.OK
         return call
 
@@ -54,7 +56,7 @@ class Calls:
 def gpu(monkeypatch):
     """(calls, made): the launches, and {address: stream that was current when the buffer was made}."""
     current, made = [CURRENT], {}
-    Gpu.recorded = []
+    Gpu.recorded, Gpu.at, Gpu.current = [], 0, 0
     calls = Calls(tbl.lib())
 
     @contextlib.contextmanager
@@ -62,6 +64,12 @@ def gpu(monkeypatch):
         current.append(current[-1] if stream is None else stream.cuda_stream)
         yield
         current.pop()
+
+    @contextlib.contextmanager
+    def on_gpu(index):
+        before, Gpu.current = Gpu.current, index
+        yield
+        Gpu.current = before
 
     def maker(make):
         def wrapped(*a, **k):
@@ -78,10 +86,11 @@ def gpu(monkeypatch):
         monkeypatch.setattr(torch, name, maker(getattr(torch, name)))
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", on_gpu)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: Gpu.current)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(current[-1]))
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: current[-1], raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: Gpu.current, raising=False)
     monkeypatch.setattr(tbl, "lib", lambda: calls)
     return calls, made
 
@@ -150,3 +159,18 @@ def test_buffers_of_a_call_on_the_current_stream(gpu, name, stream):
     assert made and set(made.values()) == {CURRENT} and Gpu.recorded == []
     (_, args), = calls.calls
     assert args[-1] == CURRENT
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n != "tile_map"])
+def test_a_call_runs_on_its_tensors_gpu(gpu, name):
+    """A default stream's address is 0 on every GPU: it means the current GPU's."""
+    calls, _ = gpu
+    Gpu.at = 1
+    CALLS[name](None)
+    assert calls.on == [1] and Gpu.current == 0
+
+
+def test_tile_map_runs_on_its_gpu(gpu):
+    calls, _ = gpu
+    tbl.tile_map(tbl.ROW, 4, 4, device="cuda:1")
+    assert calls.on == [1] and Gpu.current == 0

@@ -171,6 +171,16 @@ def _on(stream, index):
     return int(stream), torch.cuda.ExternalStream(int(stream), device=index)
 
 
+def _launch(index, fn, *args):
+    """fn(*args) with GPU ``index`` as the current one: a default stream's address is 0 on every GPU, and means the current
+    one's."""
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
 def _buffer(shape, dtype, device, side, output=True):
     """A new buffer for a call that runs on ``side`` (None: the current stream), from that stream's pool: the current
     one's hands out blocks that kernels waiting there still use. An output is recorded on the current stream, where the
@@ -246,17 +256,17 @@ def gemm(a, b, c=None, mode=ROW, group=1, persistent=False, num_programs=0, out_
         bm, bn, _ = tile if tile is not None else gemm_tile_shape(M, N, K)
         _device_tensor(trace, "trace", torch.int32, 8 * (-(-M // bm)) * (-(-N // bn)), a.device)
     if tile is None and trace is None:
-        st = lib().tbl_gemm(_ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode), int(group),
-                            int(bool(persistent)), int(num_programs), s)
+        st = _launch(a.get_device(), lib().tbl_gemm, _ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode),
+                     int(group), int(bool(persistent)), int(num_programs), s)
         _check(st, "tbl_gemm")
     else:
         if tile is None:
             bm, bn, bk = gemm_tile_shape(M, N, K)
         else:
             bm, bn, bk = tile
-        st = lib().tbl_gemm_tiled(_ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode), int(group),
-                                  int(bool(persistent)), int(num_programs), int(bm), int(bn), int(bk),
-                                  _ptr(trace), s)
+        st = _launch(a.get_device(), lib().tbl_gemm_tiled, _ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode),
+                     int(group), int(bool(persistent)), int(num_programs), int(bm), int(bn), int(bk),
+                     _ptr(trace), s)
         _check(st, "tbl_gemm_tiled")
     return c
 
@@ -311,8 +321,8 @@ def gemm_dynamic_noalloc(a, b, c=None, mode=ROW, group=1, num_programs=0, out_dt
     library call allocates nothing (``c`` is allocated here when not given). Calls that overlap in
     time on one GPU share that array and must be serialised. Returns c."""
     M, N, K, dt, c, _, s, _ = _dynamic_args(a, b, c, out_dtype, trace, stream)
-    st = lib().tbl_gemm_dynamic_noalloc(_ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode), int(group),
-                                        int(num_programs), _ptr(trace), s)
+    st = _launch(a.get_device(), lib().tbl_gemm_dynamic_noalloc, _ptr(a), _ptr(b), _ptr(c), M, N, K, dt,
+                 int(mode), int(group), int(num_programs), _ptr(trace), s)
     _check(st, "tbl_gemm_dynamic_noalloc")
     return c
 
@@ -331,8 +341,8 @@ def gemm_dynamic(a, b, c=None, mode=ROW, group=1, num_programs=0, workspace=None
         with torch.cuda.stream(side):   # None: the current one
             workspace = dynamic_workspace(P, a.device)
     _device_tensor(workspace, "workspace", torch.int32, device=a.device)
-    st = lib().tbl_gemm_dynamic(_ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode), int(group),
-                                int(num_programs), _ptr(workspace), workspace.numel(), _ptr(trace), s)
+    st = _launch(a.get_device(), lib().tbl_gemm_dynamic, _ptr(a), _ptr(b), _ptr(c), M, N, K, dt, int(mode),
+                 int(group), int(num_programs), _ptr(workspace), workspace.numel(), _ptr(trace), s)
     _check(st, "tbl_gemm_dynamic")
     return c
 
@@ -372,8 +382,8 @@ def gemm_lds_layout(a, b, layout, c=None, mode=ROW, group=1, persistent=False, n
         _device_tensor(t, name, device=a.device)
     app, amp, bv, bpp, bmp = (int(x) for x in layout)
     fn = lib().tbl_gemm_lds_layout16 if mfma16 else lib().tbl_gemm_lds_layout
-    st = fn(_ptr(a), _ptr(b), _ptr(c), M, N, K, F16, int(mode), int(group), int(bool(persistent)),
-            int(num_programs), app, amp, bv, bpp, bmp, s)
+    st = _launch(a.get_device(), fn, _ptr(a), _ptr(b), _ptr(c), M, N, K, F16, int(mode), int(group),
+                 int(bool(persistent)), int(num_programs), app, amp, bv, bpp, bmp, s)
     _check(st, "tbl_gemm_lds_layout16" if mfma16 else "tbl_gemm_lds_layout")
     return c
 
@@ -397,8 +407,8 @@ def mfma_rate(a, b, workgroups=256, iters=4000, stream=None):
     with torch.cuda.stream(side):   # None: the current one
         cycles.zero_()
     dtype = BF16 if a.dtype == torch.bfloat16 else F16
-    st = lib().tbl_mfma_rate(_ptr(a), _ptr(b), elems, dtype, int(workgroups), int(iters), _ptr(out),
-                             _ptr(cycles), s)
+    st = _launch(a.get_device(), lib().tbl_mfma_rate, _ptr(a), _ptr(b), elems, dtype, int(workgroups),
+                 int(iters), _ptr(out), _ptr(cycles), s)
     _check(st, "tbl_mfma_rate")
     flops = 2 * 32 * 32 * 16 * 16 * int(iters) * 4 * int(workgroups)
     return flops, out, cycles
@@ -470,7 +480,8 @@ def quantize_fp8(x, fmt=None, rows=1, transposed=False, stream=None):
         raise ValueError("the rows of x must be contiguous")
     rg, cg = (R + 127) // 128, (C + 127) // 128
     dev = x.device
-    address, side = _on(stream, x.get_device())
+    index = x.get_device()
+    address, side = _on(stream, index)
     codes = _buffer((R, cg * 128), fmt, dev, side)
     scale = _buffer((cg, R) if rows == 1 else (rg, cg), torch.float32, dev, side)
     codes_t = scale_t = None
@@ -478,9 +489,9 @@ def quantize_fp8(x, fmt=None, rows=1, transposed=False, stream=None):
         codes_t = _buffer((C, rg * 128), fmt, dev, side)
         scale_t = _buffer((rg, C) if rows == 1 else (cg, rg), torch.float32, dev, side)
     if R and C:
-        st = lib().tbl_quantize_fp8(x.data_ptr(), R, C, ld, xt, ft, rows, codes.data_ptr(), cg * 128, scale.data_ptr(),
-                                    codes_t.data_ptr() if transposed else None, rg * 128,
-                                    scale_t.data_ptr() if transposed else None, address)
+        st = _launch(index, lib().tbl_quantize_fp8, x.data_ptr(), R, C, ld, xt, ft, rows, codes.data_ptr(),
+                     cg * 128, scale.data_ptr(), codes_t.data_ptr() if transposed else None, rg * 128,
+                     scale_t.data_ptr() if transposed else None, address)
         if st:
             _check(st, "tbl_quantize_fp8")
     q = Fp8Blocks(codes if C == cg * 128 else codes[:, :C], scale, rows)
@@ -575,9 +586,10 @@ def gemm_fp8(a, b, add=None, out=None, out_dtype=None, workspace=None, stream=No
         workspace = _buffer(need, torch.uint8, device, side, output=False)
     if workspace is not None:
         _device_tensor(workspace, "workspace", torch.uint8, need, device)
-    st = lib().tbl_gemm_fp8(at.data_ptr(), lda, fa, a.scale.data_ptr(), a.rows, bt.data_ptr(), ldb, fb, b.scale.data_ptr(),
-                            b.rows, None if add is None else add.data_ptr(), out.data_ptr(), ot, M, N, K,
-                            None if need <= 0 else workspace.data_ptr(), 0 if need <= 0 else workspace.numel(), address)
+    st = _launch(index, lib().tbl_gemm_fp8, at.data_ptr(), lda, fa, a.scale.data_ptr(), a.rows, bt.data_ptr(),
+                 ldb, fb, b.scale.data_ptr(), b.rows, None if add is None else add.data_ptr(), out.data_ptr(),
+                 ot, M, N, K, None if need <= 0 else workspace.data_ptr(),
+                 0 if need <= 0 else workspace.numel(), address)
     if st:
         _check(st, "tbl_gemm_fp8")
     return out
@@ -618,7 +630,8 @@ def newton_schulz(x, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
         raise ValueError("the rows of x must be contiguous")
     a, b, c = (float(v) for v in coefficients)
     device = x.device
-    address, side = _on(stream, x.get_device())
+    index = x.get_device()
+    address, side = _on(stream, index)
     if out is None:
         out = _buffer(x.shape, out_dtype, device, side)
     elif out.shape != x.shape or out.dtype != out_dtype or not out.is_contiguous() or out.device != device:
@@ -627,9 +640,9 @@ def newton_schulz(x, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     if workspace is None:
         workspace = _buffer(need, torch.uint8, device, side, output=False)
     _device_tensor(workspace, "workspace", torch.uint8, need, device)
-    st = lib().tbl_newton_schulz(x.data_ptr(), batch, R, C, ld, x.stride(0) if batch > 1 else 0, x_types[x.dtype],
-                                 out.data_ptr(), x_types[out_dtype], int(steps), a, b, c, float(eps), workspace.data_ptr(),
-                                 workspace.numel(), address)
+    st = _launch(index, lib().tbl_newton_schulz, x.data_ptr(), batch, R, C, ld, x.stride(0) if batch > 1 else 0,
+                 x_types[x.dtype], out.data_ptr(), x_types[out_dtype], int(steps), a, b, c, float(eps),
+                 workspace.data_ptr(), workspace.numel(), address)
     _check(st, "tbl_newton_schulz")
     return out
 
@@ -653,14 +666,16 @@ def tile_map(mode, grid_m, grid_n, group=1, out_m=None, out_n=None, device="cuda
     device = given[0].device if given else torch.device(device)
     if device.type != "cuda":
         raise ValueError(f"out_m and out_n must be GPU tensors (got device {device})")
-    s, side = _on(stream, torch.cuda.current_device() if device.index is None else device.index)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    s, side = _on(stream, index)
     if out_m is None:
         out_m = _buffer(T, torch.int32, device, side)
     if out_n is None:
         out_n = _buffer(T, torch.int32, device, side)
     _device_tensor(out_m, "out_m", torch.int32, T)
     _device_tensor(out_n, "out_n", torch.int32, T, out_m.device)
-    st = lib().tbl_tile_map(int(mode), int(grid_m), int(grid_n), int(group), _ptr(out_m), _ptr(out_n), s)
+    st = _launch(index, lib().tbl_tile_map, int(mode), int(grid_m), int(grid_n), int(group), _ptr(out_m),
+                 _ptr(out_n), s)
     _check(st, "tbl_tile_map", allow_warning=True)
     return out_m, out_n, st
 
@@ -678,7 +693,7 @@ def transpose_i32(x, out=None, layout=T_XOR, stream=None):
     if out.shape != (cols, rows):
         raise ValueError(f"out must be ({cols}, {rows})")
     _device_tensor(out, "out", torch.int32, device=x.device)
-    st = lib().tbl_transpose_i32(_ptr(x), _ptr(out), rows, cols, int(layout), s)
+    st = _launch(x.get_device(), lib().tbl_transpose_i32, _ptr(x), _ptr(out), rows, cols, int(layout), s)
     _check(st, "tbl_transpose_i32")
     return out
 
@@ -699,7 +714,7 @@ def copy16(src, dst=None, nontemporal=False, stream=None):
     if dst.numel() * dst.element_size() != nbytes:
         raise ValueError("src and dst must hold the same number of bytes")
     _device_tensor(dst, "dst", device=src.device)
-    st = lib().tbl_copy16(_ptr(src), _ptr(dst), nbytes, 1 if nontemporal else 0, s)
+    st = _launch(src.get_device(), lib().tbl_copy16, _ptr(src), _ptr(dst), nbytes, 1 if nontemporal else 0, s)
     _check(st, "tbl_copy16")
     return dst
 
