@@ -21,7 +21,7 @@ import thread_block_lds_amd as tbl  # noqa: E402
 
 class Fp8Linear(torch.autograd.Function):
     """x (T, C) and an fp32 master weight w (N, C) -> x @ w.T in x's dtype; grad is the fp32 gradient of w that the
-    backward adds to (w itself takes no part in autograd)."""
+    backward adds to (w itself takes no part in autograd). The backward is not differentiable itself."""
 
     @staticmethod
     def forward(ctx, x, w, grad):
@@ -31,6 +31,7 @@ class Fp8Linear(torch.autograd.Function):
         return tbl.gemm_fp8(xq, wq, out_dtype=x.dtype)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         q, t = tbl.quantize_fp8(dy.contiguous(), fmt=torch.float8_e5m2, transposed=True)
         tbl.gemm_fp8(t, ctx.xt, add=ctx.grad, out=ctx.grad)

@@ -453,7 +453,8 @@ def quantize_fp8(x, fmt=None, rows=1, transposed=False, stream=None):
     fmt: torch.float8_e4m3fn (default) or torch.float8_e5m2. rows: 1, a scale for each 1 x 128 group of a row
     (activations, gradients), or 128, one for each 128 x 128 block (weights). Returns Fp8Blocks; with
     ``transposed`` a pair of them, x and its transpose, from one pass over x. The codes' rows are stored
-    at a stride of a multiple of 128 bytes, with zeros past the last column."""
+    at a stride of a multiple of 128 bytes, with zeros past the last column. Autograd does not see the call: the result
+    carries no gradient, whatever x asks for."""
     import torch
     if not _x_types:
         _types()
@@ -558,7 +559,8 @@ def gemm_fp8(a, b, add=None, out=None, out_dtype=None, workspace=None, stream=No
     add: optional fp32 (M, N), contiguous; it may be ``out`` itself (a gradient accumulated in place). out: optional
     (M, N) output, contiguous. out_dtype: torch.bfloat16 (default), float16 or float32. The formats and the
     scales' layouts of A and B may differ. workspace: a uint8 tensor of at least gemm_fp8_workspace(M, N, K)
-    bytes (default: a fresh one). Returns C."""
+    bytes (default: a fresh one). Returns C. Autograd does not see the call: a layer's backward is made of such
+    products itself (examples/train_fp8_muon.py)."""
     import torch
     x_types = _x_types or _types()[0]
     device, index = a.codes.device, a.codes.get_device()
@@ -610,7 +612,7 @@ def newton_schulz(x, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     update of the Muon optimiser).
 
     out: optional contiguous output of x's shape; out_dtype: default x's dtype. workspace: a uint8 tensor of at least
-    newton_schulz_workspace(batch, R, C) bytes (default: a fresh one). Returns the output."""
+    newton_schulz_workspace(batch, R, C) bytes (default: a fresh one). Returns the output, which carries no gradient."""
     import torch
     x_types, _ = _types()
     if x.dim() != 2 and x.dim() != 3:
