@@ -127,6 +127,12 @@ struct OrthoLaunch {
   void* work;                                // ortho_workspace bytes
 };
 int64_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols);
+// How a step's product is run (kind 0: P, 1: Q, 2: the update, 3: the last step's): its tile, 0 where a short side makes a
+// step one launch, and the parts along k that a last round's tiles are split into (1: none).
+struct OrthoProduct {
+  int tile, parts;
+};
+OrthoProduct ortho_product(int kind, int64_t batch, int64_t rows, int64_t cols);
 hipError_t launch_ortho(const OrthoLaunch& a, hipStream_t s);
 
 }  // namespace tbl

@@ -1228,6 +1228,15 @@ float pow2_below(double v) {
 
 int64_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols) { return make_plan(batch, rows, cols).bytes; }
 
+OrthoProduct ortho_product(int kind, int64_t batch, int64_t rows, int64_t cols) {
+  const OrthoPlan o = make_plan(batch, rows, cols);
+  if (o.small) return OrthoProduct{0, 1};
+  const int r = static_cast<int>(o.r), M = is_update(kind) ? static_cast<int>(o.c) : r;
+  const int K = static_cast<int>(kind == kGram ? o.ldc : o.ldr);
+  const int tile = tile_size(kind, M, r, K, batch);
+  return OrthoProduct{tile, tile == 256 ? make_deal(make_tiles(kind, M, r, 256).count * batch, K / kStep, 256).parts : 1};
+}
+
 hipError_t launch_ortho(const OrthoLaunch& l, hipStream_t s) {
   const OrthoPlan o = make_plan(l.batch, l.rows, l.cols);
   char* base = static_cast<char*>(l.work);
