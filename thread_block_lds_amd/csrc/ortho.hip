@@ -1119,26 +1119,38 @@ hipError_t product(const OrthoArgs& a, int batch, float* work, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int kType>
-void launch_norm(const OrthoLaunch& l, int parts, double* norms, hipStream_t s) {
-  const bool flat = l.ld == l.cols || l.rows == 1;   // then the matrix is one long row
-  hipLaunchKernelGGL((ortho_norm_kernel<kType>), dim3(static_cast<unsigned>(l.batch * parts)), dim3(256), 0, s, l.x, flat ? 1 : l.rows,
-                     flat ? l.rows * l.cols : l.cols, l.ld, l.batch_ld, parts, norms);
+// Parts of a matrix's norm that has ``pieces``. A launch takes less than 2^32 threads: no more than 2^20 workgroups in all.
+int norm_parts(int64_t batch, int64_t pieces) {
+  int64_t most = (int64_t{1} << 20) / batch;
+  if (most > kNormParts) most = kNormParts;
+  if (most < 1) most = 1;
+  return static_cast<int>(pieces < most ? pieces : most);
 }
 
 template <int kType>
-void launch_enter(const OrthoLaunch& l, int parts, double* norms, float kx, _Float16* straight, int64_t lds_, int64_t batch_s,
+hipError_t launch_norm(const OrthoLaunch& l, int parts, double* norms, hipStream_t s) {
+  const bool flat = l.ld == l.cols || l.rows == 1;   // then the matrix is one long row
+  hipLaunchKernelGGL((ortho_norm_kernel<kType>), dim3(static_cast<unsigned>(l.batch * parts)), dim3(256), 0, s, l.x, flat ? 1 : l.rows,
+                     flat ? l.rows * l.cols : l.cols, l.ld, l.batch_ld, parts, norms);
+  return hipGetLastError();
+}
+
+template <int kType>
+hipError_t launch_enter(const OrthoLaunch& l, int parts, double* norms, float kx, _Float16* straight, int64_t lds_, int64_t batch_s,
                   _Float16* turned, int64_t ldt, int64_t batch_t, _Float16* lo, bool lo_turned, OrthoScalars* scalars,
                   hipStream_t s) {
-  launch_norm<kType>(l, parts, norms, s);
+  const hipError_t e = launch_norm<kType>(l, parts, norms, s);
+  if (e != hipSuccess) return e;
   const dim3 grid(static_cast<unsigned>((l.cols + 63) / 64), static_cast<unsigned>((l.rows + 63) / 64), static_cast<unsigned>(l.batch));
   hipLaunchKernelGGL((ortho_enter_kernel<kType>), grid, dim3(256), 0, s, l.x, l.rows, l.cols, l.ld, l.batch_ld, parts, norms, l.eps,
                      kx, straight, lds_, batch_s, turned, ldt, batch_t, lo, lo_turned, scalars);
+  return hipGetLastError();
 }
 
 template <int kType, int kR>
 hipError_t launch_small(const OrthoLaunch& l, int parts, double* norms, SmallArgs a, float* share0, float* share1, hipStream_t s) {
-  launch_norm<kType>(l, parts, norms, s);
+  const hipError_t e = launch_norm<kType>(l, parts, norms, s);
+  if (e != hipSuccess) return e;
   const dim3 grid(static_cast<unsigned>((a.batch + kNumXcds - 1) / kNumXcds * kNumXcds) * a.chunks);
   a.p_out = share0;
   hipLaunchKernelGGL((ortho_small_enter_kernel<kType, kR>), grid, dim3(Small<kR>::kThreads), 0, s, l.x, l.ld, l.batch_ld, l.rows > l.cols, parts, l.eps, a);
@@ -1195,7 +1207,7 @@ OrthoPlan make_plan(int64_t batch, int64_t rows, int64_t cols) {
   o.lo = take(batch * (o.small ? up(o.c, 128) : o.c) * o.ldr * 2);
   int64_t parts = o.c * ((o.r + kNormSpan - 1) / kNormSpan);   // of the norm, for either orientation
   if (parts < o.r * ((o.c + kNormSpan - 1) / kNormSpan)) parts = o.r * ((o.c + kNormSpan - 1) / kNormSpan);
-  o.norms = take(batch * (parts < kNormParts ? parts : kNormParts) * 8);
+  o.norms = take(batch * norm_parts(batch, parts) * 8);
   o.scalars = take(batch * 8);
   if (o.small) {
     o.chunks = small_chunks(o.c, o.ldr, batch);
@@ -1254,7 +1266,7 @@ hipError_t launch_ortho(const OrthoLaunch& l, hipStream_t s) {
   const double most = 1.5 * __builtin_fabs(l.b) + 2.25 * __builtin_fabs(l.c);
   const float kq = most * 4096 <= 60000 ? 4096.0f : most <= 60000 ? pow2_below(60000 / most) : 1.0f;
   const int64_t pieces = l.ld == l.cols || l.rows == 1 ? (l.rows * l.cols + kNormSpan - 1) / kNormSpan : l.rows * ((l.cols + kNormSpan - 1) / kNormSpan);
-  const int parts = static_cast<int>(pieces < kNormParts ? pieces : kNormParts);
+  const int parts = norm_parts(l.batch, pieces);
   float* part_work = reinterpret_cast<float*>(base + o.parts);
   if (o.small) {
     SmallArgs a{};
@@ -1289,12 +1301,12 @@ hipError_t launch_ortho(const OrthoLaunch& l, hipStream_t s) {
   _Float16* lo0 = l.dtype == 2 ? lo : nullptr;   // 16-bit inputs have no remainder
   _Float16 *straight = tall ? u0 : w, *turned = tall ? w : u0;
   const int64_t ls = tall ? o.ldr : o.ldc, lt = tall ? o.ldc : o.ldr, bs = tall ? bu : bw, bt = tall ? bw : bu;
+  hipError_t e;
   switch (l.dtype) {
-    case 0: launch_enter<0>(l, parts, norms, kx, straight, ls, bs, turned, lt, bt, lo0, !tall, scalars, s); break;
-    case 1: launch_enter<1>(l, parts, norms, kx, straight, ls, bs, turned, lt, bt, lo0, !tall, scalars, s); break;
-    default: launch_enter<2>(l, parts, norms, kx, straight, ls, bs, turned, lt, bt, lo0, !tall, scalars, s); break;
+    case 0: e = launch_enter<0>(l, parts, norms, kx, straight, ls, bs, turned, lt, bt, lo0, !tall, scalars, s); break;
+    case 1: e = launch_enter<1>(l, parts, norms, kx, straight, ls, bs, turned, lt, bt, lo0, !tall, scalars, s); break;
+    default: e = launch_enter<2>(l, parts, norms, kx, straight, ls, bs, turned, lt, bt, lo0, !tall, scalars, s); break;
   }
-  hipError_t e = hipGetLastError();
   for (int i = 0; i < l.steps && e == hipSuccess; ++i) {
     OrthoArgs g{};
     g.A = w; g.B = w; g.lda = g.ldb = o.ldc; g.batch_a = g.batch_b = bw;
