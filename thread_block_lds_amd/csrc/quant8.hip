@@ -169,6 +169,17 @@ __device__ __forceinline__ uint2 code_eight(const Eight<kType>& v, const Coder<k
   return make_uint2(pack4<kFmt>(q[0], q[1], q[2], q[3]), pack4<kFmt>(q[4], q[5], q[6], q[7]));
 }
 
+// Which of eight neighbouring codes stand for values that exist, the first n; the others are written as codes of 0, also where
+// the group's NaN would make NaN of them.
+struct Kept {
+  uint2 mask;
+  __device__ __forceinline__ explicit Kept(int64_t n) {
+    const uint64_t m = n >= 8 ? ~uint64_t{0} : n <= 0 ? 0 : (uint64_t{1} << (8 * n)) - 1;
+    mask = make_uint2(static_cast<uint32_t>(m), static_cast<uint32_t>(m >> 32));
+  }
+  __device__ __forceinline__ uint2 of(uint2 w) const { return make_uint2(w.x & mask.x, w.y & mask.y); }
+};
+
 // Groups of 1 x 128, one direction: 16 lanes a group, a workgroup takes 16 rows x kSpan consecutive groups and
 // has all its loads in flight at once. One row of 4096 takes 3.8 us, a launch's own time.
 constexpr int kSpan = 4;
@@ -194,7 +205,8 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const typename In<kType
     const float most = most_value<kType>(max16(most_of<kType>(v[s])));
     Coder<kType, kFmt> k;
     k.set(most);
-    *reinterpret_cast<uint2*>(codes + row * ldc + (g0 + s) * kGroup + 8 * lane16) = code_eight<kType, kFmt>(v[s], k);
+    const int64_t c = (g0 + s) * kGroup + 8 * lane16;
+    *reinterpret_cast<uint2*>(codes + row * ldc + c) = Kept(cols - c).of(code_eight<kType, kFmt>(v[s], k));
     if (lane16 == 0) scale[(g0 + s) * rows + row] = most / kMost[kFmt];
   }
 }
@@ -229,6 +241,7 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const typename In<kType
     }
   }
 
+  const Kept in_cols(cols - c0 - 8 * cg), in_rows(rows - r0 - 8 * rg);
   uint2 turned[8];   // the codes of this thread's columns, eight rows each
   if constexpr (kBlock == 1) {
 #pragma unroll
@@ -237,7 +250,7 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const typename In<kType
       const float most = most_value<kType>(max16(most_of<kType>(v[i])));
       Coder<kType, kFmt> k;
       k.set(most);
-      const uint2 w = code_eight<kType, kFmt>(v[i], k);
+      const uint2 w = in_cols.of(code_eight<kType, kFmt>(v[i], k));
       if (row < rows) {
         *reinterpret_cast<uint2*>(codes + row * ldc + c0 + 8 * cg) = w;
         if (cg == 0) scale[blockIdx.x * rows + row] = most / kMost[kFmt];
@@ -269,7 +282,7 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const typename In<kType
         float q[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) q[i] = k.quotient(v[i].value(e));
-        turned[e] = make_uint2(pack4<kFmt>(q[0], q[1], q[2], q[3]), pack4<kFmt>(q[4], q[5], q[6], q[7]));
+        turned[e] = in_rows.of(make_uint2(pack4<kFmt>(q[0], q[1], q[2], q[3]), pack4<kFmt>(q[4], q[5], q[6], q[7])));
         if (rg == 0 && c0 + col < cols) scale_t[blockIdx.y * cols + c0 + col] = most / kMost[kFmt];
       }
     }
@@ -289,7 +302,7 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const typename In<kType
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t row = r0 + 8 * rg + i;
-      w[i] = code_eight<kType, kFmt>(v[i], k);
+      w[i] = in_cols.of(code_eight<kType, kFmt>(v[i], k));
       if (row < rows) *reinterpret_cast<uint2*>(codes + row * ldc + c0 + 8 * cg) = w[i];
     }
     if (t == 0) {
@@ -308,7 +321,7 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const typename In<kType
             const uint32_t a = h ? w[2 * p].y : w[2 * p].x, b = h ? w[2 * p + 1].y : w[2 * p + 1].x;
             lo[p] = __builtin_amdgcn_perm(a, b, sel);   // byte 0: a's byte e, byte 1: b's byte e
           }
-          turned[4 * h + e] = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+          turned[4 * h + e] = in_rows.of(make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
         }
     }
   }
