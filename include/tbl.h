@@ -462,7 +462,9 @@ int tbl_quantize_fp8(const void* x, int64_t rows, int64_t cols, int64_t ldx, int
  *   workspace     device memory of tbl_gemm_fp8_workspace(M, N, K) bytes, 16-byte aligned (NULL when that is 0)
  * Between groups sums are fp32. Within a group, 16-bit outputs use the 8-bit matrix instructions, which sum eight
  * products at a time and keep each to 2^-13 of the largest of the eight; fp32 outputs take products of the codes
- * as fp16 (exact), summed in fp32.
+ * as fp16 (exact), summed in fp32. Two scales are multiplied in fp32 first; where finite ones have a product beyond its
+ * largest value, the group's sum is multiplied by the smaller and then by the larger, and a product below 2^-126 has a
+ * subnormal's bits.
  * The result does not depend on anything but the arguments: the sums are taken in one order.
  * Sizes 0 .. 2^20. M or N 0: nothing is enqueued; K 0: C = add, or 0.
  */

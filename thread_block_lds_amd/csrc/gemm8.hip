@@ -251,6 +251,89 @@ __device__ __forceinline__ void add_scaled(f32x4_t& acc, const f32x4_t& p, float
   for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(p[e], kRowB ? sa * sb4[e] : sb, acc[e]);
 }
 
+// Whether two finite scales have a product beyond fp32: then a group's sum of 0 would become NaN and a small one infinite.
+__device__ __forceinline__ bool beyond(float sa, float sb) {
+  constexpr float inf = __builtin_huge_valf();
+  return __builtin_fabsf(sa) < inf && __builtin_fabsf(sb) < inf && !(__builtin_fabsf(sa * sb) < inf);
+}
+// add_scaled, where scales may be beyond: those sums are taken by the smaller scale first.
+template <bool kRowB>
+__device__ __forceinline__ void add_scaled_wide(f32x4_t& acc, const f32x4_t& p, float sa, float sb, const f32x4_t& sb4) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float s = kRowB ? sb4[e] : sb;
+    const bool wide = beyond(sa, s), less = __builtin_fabsf(s) < __builtin_fabsf(sa);
+    acc[e] = wide ? __builtin_fmaf(p[e] * (less ? s : sa), less ? sa : s, acc[e]) : __builtin_fmaf(p[e], sa * s, acc[e]);
+  }
+}
+
+// The loops take the product of two scales first, one multiplication a row and group instead of one a result. Where a wave's sums
+// (groups g0, g0 + step, ... below g1, of the rows from m0 and columns from n0, which began at start(i, j)) are not all finite
+// and a group of theirs has scales beyond fp32 together, they are taken again from memory with add_scaled_wide. Sums that are
+// not finite for another reason, a NaN or an infinity in a row, cost the look at the scales.
+template <int kFa, int kFb, bool kRowB, bool kExact, int TM, int TN, class Start>
+__device__ __forceinline__ void mend_range(const Gemm8Args& a, int g0, int g1, int step, int m0, int n0, f32x4_t (&acc)[TM][TN], Start start) {
+  constexpr float inf = __builtin_huge_valf();
+  float top = 0;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = __builtin_elementwise_maximum(top, __builtin_fabsf(acc[i][j][e]));   // a NaN stays
+  if (__builtin_amdgcn_ballot_w64(!(top < inf)) == 0) return;
+  const int r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+  auto scale_a = [&](int m, int g) { return a.sa[(min(m, a.M - 1) >> a.a_shift) * a.sa_row + g * a.sa_group]; };
+  auto scale_b = [&](int n, int g) { return a.sb[(min(n, a.N - 1) >> a.b_shift) * a.sb_row + g * a.sb_group]; };
+  bool wide = false;
+#pragma unroll 1
+  for (int g = g0; g < g1; g += step) {
+    float most = 0;   // of this lane's rows' finite scales
+#pragma unroll 1
+    for (int i = 0; i < TM; ++i) {
+      const float s = __builtin_fabsf(scale_a(m0 + 16 * i + r, g));
+      if (s < inf) most = __builtin_fmaxf(most, s);
+    }
+#pragma unroll 1
+    for (int n = 0; n < (kRowB ? 4 * TN : 1); ++n) wide |= beyond(most, scale_b(n0 + (kRowB ? 16 * (n >> 2) + 4 * q + (n & 3) : 0), g));
+  }
+  if (__builtin_amdgcn_ballot_w64(wide) == 0) return;
+  auto fetch = [&](const uint8_t* p, int64_t ld, int row, int rows, int g) -> Codes {   // this lane's two chunks of a row
+    uint4 c[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = g * kGroup + 64 * h + 16 * q;
+      c[h] = make_uint4(0, 0, 0, 0);
+      if (row < rows && k < a.K) c[h] = keep_bytes(*reinterpret_cast<const uint4*>(p + row * ld + k), a.K - k);
+    }
+    return Codes{c[0], c[1]};
+  };
+  // a row block at a time, with few registers: the sums of all of them are live
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = start(i, j);
+#pragma unroll 1
+    for (int g = g0; g < g1; g += step) {
+      Operand<kFa, kExact> av;
+      av.set(fetch(a.A, a.lda, m0 + 16 * i + r, a.M, g));
+      const float sa = scale_a(m0 + 16 * i + r, g), sb = scale_b(n0, g);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        Operand<kFb, kExact> bv;
+        bv.set(fetch(a.B, a.ldb, n0 + 16 * j + r, a.N, g));
+        f32x4_t sb4 = {sb, sb, sb, sb};
+        if constexpr (kRowB) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sb4[e] = scale_b(n0 + 16 * j + 4 * q + e, g);
+        }
+        add_scaled_wide<kRowB>(acc[i][j], product<kFa, kFb>(bv, av), sa, sb, sb4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+}
+
 // 256 x 256 tiles with the two-group loop of nt_tile.hpp (16-bit outputs). The scales have four slots of their own in
 // LDS and are read with the operands. A compute half-period is 16 matrix instructions of 32 cycles; the
 // 4 multiply-adds (kRowB: 4 products too) that follow each run beside the next one. 8192^3: 411 to 440 us, 2.5 to 2.67 PFLOP/s,
@@ -447,6 +530,7 @@ __global__ __launch_bounds__(kNtThreads) void gemm8_tile256_kernel(Gemm8Args a, 
     multiply(4);
     settle(4);
   }
+  mend_range<kFa, kFb, kRowB, false>(a, share.s0, share.s1, 1, tm * 256 + t.wm * 128, tn * 256 + t.wn * 64, acc, [](int, int) { return f32x4_t{0, 0, 0, 0}; });
   if (share.unit >= 0) {
     write_part(deal, work, share.unit, t.wave, t.lane, a.M - tm * 256 - t.wm * 128, acc);
     return;
@@ -525,8 +609,8 @@ __global__ __launch_bounds__(kNtThreads) void gemm8_tile128_kernel(Gemm8Args a, 
   auto clear_tail = [&](int g) {
     if ((tail & 15) == 0 || g != last) return;
     if (threadIdx.x < 256) {
-    char* p = lds + (g & (kNt128Stages - 1)) * kNt128Stage + threadIdx.x * kNtRow + (((tail >> 4) ^ (threadIdx.x >> 1)) & 7) * 16;
-    *reinterpret_cast<uint4*>(p) = keep_bytes(*reinterpret_cast<uint4*>(p), tail & 15);
+      char* p = lds + (g & (kNt128Stages - 1)) * kNt128Stage + threadIdx.x * kNtRow + (((tail >> 4) ^ (threadIdx.x >> 1)) & 7) * 16;
+      *reinterpret_cast<uint4*>(p) = keep_bytes(*reinterpret_cast<uint4*>(p), tail & 15);
     }
     lds_barrier();
   };
@@ -611,6 +695,7 @@ __global__ __launch_bounds__(kNtThreads) void gemm8_tile128_kernel(Gemm8Args a, 
     for (int n = 8 - kBehind; n < 8; ++n) add(n, sc[1]);
   }
   wait_loads<0>();   // no direct load may still be writing this workgroup's LDS
+  mend_range<kFa, kFb, kRowB, false>(a, share.s0, share.s1, 1, tm * 128 + t.wm * 32, tn * 128 + t.wn * 64, acc, [](int, int) { return f32x4_t{0, 0, 0, 0}; });
   if (share.unit >= 0) {
     write_part(deal, work, share.unit, t.wave, t.lane, a.M - tm * 128 - t.wm * 32, acc);
     return;
@@ -671,12 +756,12 @@ __global__ __launch_bounds__(256, 2) void gemm8_exact_kernel(Gemm8Args a, TileOr
   issue(share.s0);
   // a whole tile's sums start from what is added: its loads then wait together with the first group's
   const int m0 = tm * 128 + wm * 64 + r, n0 = tn * 128 + wn * 64 + 4 * q;
-  const bool start = a.add != nullptr && share.unit < 0;
+  auto start = [&](int i, int j) { return a.add != nullptr && share.unit < 0 ? added(a, m0 + i * 16, n0 + j * 16) : f32x4_t{0, 0, 0, 0}; };
   f32x4_t acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = start ? added(a, m0 + i * 16, n0 + j * 16) : f32x4_t{0, 0, 0, 0};
+    for (int j = 0; j < 4; ++j) acc[i][j] = start(i, j);
   for (int g = share.s0; g < share.s1; ++g) {
     wait_loads<0>();                 // this wave's loads of group g have landed
     lds_barrier();                   // everybody's have, and nobody still reads the stage that the next loads fill
@@ -738,6 +823,7 @@ __global__ __launch_bounds__(256, 2) void gemm8_exact_kernel(Gemm8Args a, TileOr
     }
   }
   wait_loads<0>();   // no direct load may still be writing this workgroup's LDS
+  mend_range<kFa, kFb, kRowB, true>(a, share.s0, share.s1, 1, tm * 128 + wm * 64, tn * 128 + wn * 64, acc, start);
   if (share.unit >= 0) {             // as two of the joining kernel's waves of 32 rows
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -786,9 +872,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void gemm8_stream_kernel(Gemm8Ar
   for (int i = 0; i < kMB; ++i) sa[i] = a.sa + (min(16 * i + r, a.M - 1) >> a.a_shift) * a.sa_row;
   sb = a.sb + (n0 >> a.b_shift) * a.sb_row;   // kRowB: row n0's, else the block's
 
-  f32x4_t acc[kMB];
+  f32x4_t acc[kMB][1];
 #pragma unroll
-  for (int i = 0; i < kMB; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+  for (int i = 0; i < kMB; ++i) acc[i][0] = f32x4_t{0, 0, 0, 0};
   // this lane's 32 values of a group: two neighbouring chunks
   auto fetch = [&](__amdgpu_buffer_rsrc_t rs, unsigned at, int g) -> Codes {   // kNtOut and more stays past every range
     const int k = g * kGroup + 32 * q;
@@ -838,12 +924,13 @@ __global__ __launch_bounds__(kStreamWaves * 64) void gemm8_stream_kernel(Gemm8Ar
       for (int i = 0; i < kMB; ++i) {
         Operand<kFa, kF32> av;
         av.set(ac[d][i]);
-        add_scaled<kRowB>(acc[i], product<kFa, kFb>(b, av), as[d][i], as[d][i] * bs[d], bs4[d]);
+        add_scaled<kRowB>(acc[i][0], product<kFa, kFb>(b, av), as[d][i], as[d][i] * bs[d], bs4[d]);
       }
     }
   }
+  mend_range<kFa, kFb, kRowB, kF32>(a, wave, a.groups, kStreamWaves, 0, n0, acc, [](int, int) { return f32x4_t{0, 0, 0, 0}; });
 #pragma unroll
-  for (int i = 0; i < kMB; ++i) *reinterpret_cast<f32x4_t*>(&sums[wave][i][4 * lane]) = acc[i];
+  for (int i = 0; i < kMB; ++i) *reinterpret_cast<f32x4_t*>(&sums[wave][i][4 * lane]) = acc[i][0];
   __syncthreads();
   if (wave < kMB) {
     f32x4_t v = {0, 0, 0, 0};

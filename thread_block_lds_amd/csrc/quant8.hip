@@ -347,7 +347,8 @@ hipError_t launch_typed(const Quant8Launch& a, hipStream_t s) {
   const unsigned cg = static_cast<unsigned>((a.cols + kGroup - 1) / kGroup), rg = static_cast<unsigned>((a.rows + kGroup - 1) / kGroup);
   const bool both = a.codes_t != nullptr;
   if (a.block == 1 && !both) {
-    const dim3 grid((cg + kSpan - 1) / kSpan * static_cast<unsigned>((a.rows + 15) / 16));   // 2^24, a launch's most, are 412 GB of values and codes
+    // 2^24 workgroups, a launch's most, are 412 GB of values and codes
+    const dim3 grid((cg + kSpan - 1) / kSpan * static_cast<unsigned>((a.rows + 15) / 16));
     hipLaunchKernelGGL((quant_rows_kernel<kType, kFmt, kRagged>), grid, dim3(256), 0, s, x, a.rows, a.cols, a.ld, a.codes, a.ldc, a.scale);
   } else if (a.block == 1) {
     hipLaunchKernelGGL((quant_tile_kernel<kType, kFmt, 1, true, kRagged>), dim3(cg, rg), dim3(256), 0, s, x, a.rows, a.cols, a.ld,
