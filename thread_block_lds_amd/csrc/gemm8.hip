@@ -205,22 +205,13 @@ __device__ __forceinline__ void put_rows(const Gemm8Args& a, char* tile, int m0,
         *tile_four(tile, 16 * i + r, 16 * j + 4 * q) = make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
       }
     tile_fence();
-    tile_store<2>(tile, static_cast<uint16_t*>(a.C), a.N, a.M, a.N, m0 + 16 * i0, n0);
+    tile_store<2>(tile, static_cast<uint16_t*>(a.C), a.N, a.M, a.N, m0 + 16 * i0, n0, threadIdx.x & 63);
     tile_fence();
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
 // ---- tiles -----------------------------------------------------------------------------------------
-
-// 4 bytes per lane from desc + voffset into LDS: lane l writes lds_addr + 4 l.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void load4_to_lds(i32x4_t desc, unsigned lds_addr, int voffset) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :: "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voffset), "s"(desc) : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 // What a wave's scales are: 64 rows of A's (the first half of the waves) or of B's, one load of 4 bytes a lane and step.
 struct ScaleLoad {

@@ -65,6 +65,15 @@ __device__ __forceinline__ void load_to_lds_at(i32x4_t desc, unsigned base, int 
 }
 #pragma clang diagnostic pop
 
+// 4 bytes per lane from desc + voffset into LDS: lane l writes lds_addr + 4 l.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load4_to_lds(i32x4_t desc, unsigned lds_addr, int voffset) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voffset), "s"(desc) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // This wave's direct loads and LDS reads of a tile. lda, ldb in bytes.
 struct NtTile {
   int lane, wave, wm, wn;
@@ -162,8 +171,8 @@ __device__ __forceinline__ void tile_fence() {
 }
 // The tile's rows to rows m0 .. of ``to`` (rows of ld), columns n0 .. + 63; ``rows`` and ``cols`` of them exist.
 template <int TM>
-__device__ __forceinline__ void tile_store(char* tile, uint16_t* to, int64_t ld, int rows, int64_t cols, int m0, int n0) {
-  const int lane = threadIdx.x & 63, n = n0 + 8 * (lane & 7);
+__device__ __forceinline__ void tile_store(char* tile, uint16_t* to, int64_t ld, int rows, int64_t cols, int m0, int n0, int lane) {
+  const int n = n0 + 8 * (lane & 7);
 #pragma unroll
   for (int k = 0; k < 2 * TM; ++k) {
     const int row = 8 * k + (lane >> 3), m = m0 + row;

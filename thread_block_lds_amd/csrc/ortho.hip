@@ -191,6 +191,8 @@ struct OrthoArgs {
   int64_t ldc, batch_c;
   _Float16* T;           // the transpose of D, N x M, rows of ldt: kUpdate the new W; kGram, kSquare D itself (of
   int64_t ldt, batch_t;  // the tiles above the diagonal the mirror images)
+  const float* d_in;     // kSquare: what rounding took from P's diagonal, ldc of each matrix; kUpdate: from Q's
+  float* d_out;          // kGram, kSquare: from D's own
   void* out;             // kLast: the result, M x N or (out_turned) N x M, instead of D and T
   int out_type, out_turned;
   float out_factor;
@@ -198,12 +200,19 @@ struct OrthoArgs {
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
+// This lane, hidden from the compiler: it otherwise computes the addresses of all of a wave's sub-tiles once, and spills.
+__device__ __forceinline__ int hidden_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // A wave's 16 TM x 64 sub-tile of 16-bit values turned through LDS: ``tile`` (2 KiB a row block, this wave's alone) holds it
 // row-major, 128 bytes a row, 16-byte chunk c of row m at c XOR (m / 2 mod 8). Writes rows n0 .. + 63 of ``to`` (rows of ld,
 // ``rows`` and ``cols`` of them exist), columns m0 .. The transposing LDS read gives a lane four rows of its column.
 template <int TM>
-__device__ __forceinline__ void write_turned(char* tile, uint16_t* to, int64_t ld, int rows, int cols, int n0, int m0) {
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void write_turned(char* tile, uint16_t* to, int64_t ld, int rows, int cols, int n0, int m0, int lane) {
+  const int i = lane & 15, g = lane >> 4;
   constexpr int kAt = TM == 1 ? 2 : 4;   // groups of eight rows a pass: with one row block the others take more columns
 #pragma unroll
   for (int p = 0; p < (TM == 1 ? 2 : 2 * TM); ++p) {
@@ -237,8 +246,7 @@ __device__ __forceinline__ void write_turned(char* tile, uint16_t* to, int64_t l
 template <int TM>
 struct Rows {
   uint4 v[2 * TM];
-  __device__ __forceinline__ void fetch(const _Float16* p, int64_t ld, int m0, int n0, int M) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ void fetch(const _Float16* p, int64_t ld, int m0, int n0, int M, int lane) {
     const int rows = n0 < ld ? min(16 * TM, M - m0) : 0;   // ld is a multiple of 64: the 64 columns exist or do not
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<_Float16*>(p + static_cast<int64_t>(m0) * ld), 0, rows > 0 ? rows * static_cast<int>(ld) * 2 : 0, 0x00020000);
@@ -258,24 +266,45 @@ struct Old {
   Rows<TM> c, lo;
   __device__ __forceinline__ void fetch(const OrthoArgs& a, int b, int m0, int n0) {
     if constexpr (kKind == kGram) return;
-    c.fetch(a.C + b * a.batch_c, a.ldc, m0, n0, a.M);
+    const int lane = hidden_lane();
+    c.fetch(a.C + b * a.batch_c, a.ldc, m0, n0, a.M, lane);
     if constexpr (is_update(kKind)) {
-      if (a.lo_in != nullptr) lo.fetch(a.lo_in + b * a.batch_c, a.ldc, m0, n0, a.M);
+      if (a.lo_in != nullptr) lo.fetch(a.lo_in + b * a.batch_c, a.ldc, m0, n0, a.M, lane);
       else lo.clear();
     }
   }
 };
 
+// What rounding took from the diagonals of P or Q, for a wave's columns and (kSquare) rows, in LDS: this wave's alone. Issued
+// before the loop, whose waits then cover the loads.
+struct Kept {
+  const float *rows, *cols;
+  template <int kKind, int kRows>
+  __device__ __forceinline__ void fetch(const OrthoArgs& a, int b, int m0, int n0, float* lds) {
+    cols = lds;
+    rows = lds + 64;
+    if constexpr (kKind != kGram) {
+      const int lane = threadIdx.x & 63;
+      const i32x4_t desc = make_desc(a.d_in + b * a.ldc, ((a.N + 15) & ~15) * 4);   // of whole blocks; past them the rest is 0
+      load4_to_lds(desc, lds_address(reinterpret_cast<const char*>(lds)), (n0 + lane) * 4);
+      if constexpr (kKind == kSquare) {
+#pragma unroll
+        for (int m = 0; m < kRows; m += 64) load4_to_lds(desc, lds_address(reinterpret_cast<const char*>(lds + 64 + m)), (m0 + m + lane) * 4);
+      }
+    }
+  }
+  static constexpr int size(int rows) { return 64 + (rows + 63) / 64 * 64; }   // floats of a wave
+};
+
 template <int TM>
-__device__ __forceinline__ void tile_put(char* tile, const Rows<TM>& rows) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void tile_put(char* tile, const Rows<TM>& rows, int lane) {
 #pragma unroll
   for (int k = 0; k < 2 * TM; ++k) *reinterpret_cast<uint4*>(tile_chunk(tile, 8 * k + (lane >> 3), lane & 7)) = rows.v[k];
 }
 // A row block of fp32 results through the tile (4 KiB: 256 bytes a row, 16-byte chunk c of row m at c XOR m) to ``out``,
 // M x N or turned. The loops stay loops: unrolled, all their addresses are kept at once and spill.
-__device__ __forceinline__ void store_f32(char* tile, float* out, int M, int N, bool turned, int m0, int n0, const f32x4_t (&v)[4]) {
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void store_f32(char* tile, float* out, int M, int N, bool turned, int m0, int n0, const f32x4_t (&v)[4], int lane) {
+  const int i = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4_t*>(tile + i * 256 + (((4 * j + g) ^ i) << 4)) = v[j];
   tile_fence();
@@ -293,13 +322,27 @@ __device__ __forceinline__ void store_f32(char* tile, float* out, int M, int N, 
   tile_fence();
 }
 
+// f(i, j, e) for the blocks of a wave's sub-tile that lie on the matrix's diagonal; its elements are those of r = 4 q + e.
+template <int TM, class F>
+__device__ __forceinline__ void on_diagonal(int m0, int n0, F f) {
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (m0 + 16 * i == n0 + 16 * j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(i, j, e);
+      }
+}
+
 // The epilogue of a wave's sub-tile whose first row and column are m0 and n0. mirror: kGram, kSquare also write the
 // transpose. tile: 4 KiB of LDS, this wave's alone, through which values pass between whole rows in memory and
 // the matrix instructions' layout (lane: row lane mod 16 of a block, columns 4 (lane / 16) .. + 3).
 template <int kKind, int TM>
 __device__ __forceinline__ void finish(const OrthoArgs& a, int b, int m0, int n0, bool mirror, char* tile, f32x4_t (&acc)[TM][4],
-                                       const Old<kKind, TM>& old) {
-  const int r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+                                       const Old<kKind, TM>& old, const Kept& kept) {
+  const int lane = hidden_lane();
+  const int r = lane & 15, q = lane >> 4;
   float f1 = a.f1, f2 = a.f2;
   if (a.scalars != nullptr) {
     if constexpr (kKind == kGram) f1 = a.scalars[b].p;
@@ -308,7 +351,9 @@ __device__ __forceinline__ void finish(const OrthoArgs& a, int b, int m0, int n0
       f2 *= a.scalars[b].x;
     }
   }
-  // v = f1 acc, or f1 (old + its remainder) + f2 acc
+  // v = f1 acc, or f1 (old + its remainder) + f2 acc. Of P and Q the diagonals' roundings are kept: where the singular values are
+  // alike, as of a wide random matrix, the diagonal's entries are too, and one rounding of them all shifts every singular value
+  // (512 x 16384 to fp32 1.9e-3 off, with them 4.5e-4). With P = F + D, P P = F F + D F + F D; with Q = G + E, U Q = U G + U E.
   if constexpr (kKind == kGram) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -317,24 +362,40 @@ __device__ __forceinline__ void finish(const OrthoArgs& a, int b, int m0, int n0
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] *= f1;
   } else {
-    auto combine = [&](const Rows<TM>& rows, float scale) {
-      tile_put<TM>(tile, rows);
+    // f1 + f2 D of this lane's columns of block j, and f2 D of its row of block i
+    auto across = [&](int j) {
+      f32x4_t v = *reinterpret_cast<const f32x4_t*>(kept.cols + 16 * j + 4 * q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f2, v[e], f1);
+      return v;
+    };
+    auto combine = [&](const Rows<TM>& rows, float scale, auto factors) {
+      tile_put<TM>(tile, rows, lane);
       tile_fence();
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+      for (int j = 0; j < 4; ++j) {
+        const f32x4_t f = factors(j);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < TM; ++i) {
           const half4_t v = __builtin_bit_cast(half4_t, *tile_four(tile, 16 * i + r, 16 * j + 4 * q));
+          float down = 0;
+          if constexpr (kKind == kSquare) down = f2 * kept.rows[16 * i + r];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(f1, static_cast<float>(v[e]), scale * acc[i][j][e]);
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(kKind == kSquare ? f[e] + down : f[e], static_cast<float>(v[e]), scale * acc[i][j][e]);
         }
+      }
       tile_fence();
     };
     if (is_update(kKind) && a.lo_in != nullptr) {   // the remainder first: it is the smaller
-      combine(old.lo, f2);
-      f2 = 1.0f;
+      combine(old.lo, f2, [&](int) { return f32x4_t{f1, f1, f1, f1}; });
+      combine(old.c, 1.0f, across);
+    } else {
+      combine(old.c, f2, across);
     }
-    combine(old.c, f2);
+    if constexpr (kKind == kSquare)
+      on_diagonal<TM>(m0, n0, [&](int i, int j, int e) {
+        if (r == 4 * q + e) acc[i][j][e] = __builtin_fmaf(f1, kept.rows[16 * i + r], acc[i][j][e]);
+      });
   }
 
   if constexpr (kKind == kLast) {
@@ -345,7 +406,7 @@ __device__ __forceinline__ void finish(const OrthoArgs& a, int b, int m0, int n0
         f32x4_t v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = acc[i][j] * a.out_factor;
-        store_f32(tile, static_cast<float*>(a.out) + o, a.M, a.N, a.out_turned, m0 + 16 * i, n0, v);
+        store_f32(tile, static_cast<float*>(a.out) + o, a.M, a.N, a.out_turned, m0 + 16 * i, n0, v, lane);
       }
       return;
     }
@@ -361,8 +422,8 @@ __device__ __forceinline__ void finish(const OrthoArgs& a, int b, int m0, int n0
       }
     tile_fence();
     uint16_t* out = static_cast<uint16_t*>(a.out) + o;
-    if (a.out_turned) write_turned<TM>(tile, out, a.M, a.N, a.M, n0, m0);
-    else tile_store<TM>(tile, out, a.N, a.M, a.N, m0, n0);
+    if (a.out_turned) write_turned<TM>(tile, out, a.M, a.N, a.M, n0, m0, lane);
+    else tile_store<TM>(tile, out, a.N, a.M, a.N, m0, n0, lane);
   } else {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -372,13 +433,18 @@ __device__ __forceinline__ void finish(const OrthoArgs& a, int b, int m0, int n0
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           h[e] = static_cast<_Float16>(acc[i][j][e]);
-          if constexpr (kKind == kUpdate) acc[i][j][e] -= static_cast<float>(h[e]);   // the remainder
+          acc[i][j][e] -= static_cast<float>(h[e]);   // the remainder
         }
         *tile_four(tile, 16 * i + r, 16 * j + 4 * q) = __builtin_bit_cast(uint2, h);
       }
+    if constexpr (kKind != kUpdate)
+      on_diagonal<TM>(m0, n0, [&](int i, int j, int e) {
+        const int n = n0 + 16 * j + 4 * q + e;
+        if (r == 4 * q + e && n < a.ldc) a.d_out[b * a.ldc + n] = acc[i][j][e];
+      });
     tile_fence();
-    tile_store<TM>(tile, reinterpret_cast<uint16_t*>(a.D) + b * a.batch_c, a.ldc, a.M, a.ldc, m0, n0);
-    if (kKind == kUpdate || mirror) write_turned<TM>(tile, reinterpret_cast<uint16_t*>(a.T) + b * a.batch_t, a.ldt, a.N, a.M, n0, m0);
+    tile_store<TM>(tile, reinterpret_cast<uint16_t*>(a.D) + b * a.batch_c, a.ldc, a.M, a.ldc, m0, n0, lane);
+    if (kKind == kUpdate || mirror) write_turned<TM>(tile, reinterpret_cast<uint16_t*>(a.T) + b * a.batch_t, a.ldt, a.N, a.M, n0, m0, lane);
     if (kKind == kUpdate && a.lo_out != nullptr) {
       tile_fence();
 #pragma unroll
@@ -391,7 +457,7 @@ __device__ __forceinline__ void finish(const OrthoArgs& a, int b, int m0, int n0
           *tile_four(tile, 16 * i + r, 16 * j + 4 * q) = __builtin_bit_cast(uint2, l);
         }
       tile_fence();
-      tile_store<TM>(tile, reinterpret_cast<uint16_t*>(a.lo_out) + b * a.batch_c, a.ldc, a.M, a.ldc, m0, n0);
+      tile_store<TM>(tile, reinterpret_cast<uint16_t*>(a.lo_out) + b * a.batch_c, a.ldc, a.M, a.ldc, m0, n0, lane);
     }
   }
 }
@@ -433,6 +499,7 @@ __device__ __forceinline__ void tile_of(const Tiles& t, int id, int& tm, int& tn
 template <int kKind>
 __global__ __launch_bounds__(kNtThreads) void ortho_product128_kernel(OrthoArgs a, Tiles tiles) {
   __shared__ __attribute__((aligned(1024))) char lds[kNt128Stages * kNt128Stage];
+  __shared__ __attribute__((aligned(16))) float diagonals[8][Kept::size(32)];
   const int b = static_cast<int>(blockIdx.x) / tiles.count;
   int tm, tn;
   tile_of(tiles, static_cast<int>(blockIdx.x) - b * tiles.count, tm, tn);
@@ -442,6 +509,8 @@ __global__ __launch_bounds__(kNtThreads) void ortho_product128_kernel(OrthoArgs 
   // latency would show at the end
   Old<kKind, 2> old;
   old.fetch(a, b, tm * 128 + t.wm * 32, tn * 128 + t.wn * 64);
+  Kept kept;
+  kept.fetch<kKind, 32>(a, b, tm * 128 + t.wm * 32, tn * 128 + t.wn * 64, diagonals[t.wave]);
   const int steps = a.K / kStep;
   NtOperand oa, ob;
   oa.start(a.A + b * a.batch_a + static_cast<int64_t>(tm) * 128 * a.lda, min(128, a.M - tm * 128) * a.lda * 2);
@@ -501,7 +570,7 @@ __global__ __launch_bounds__(kNtThreads) void ortho_product128_kernel(OrthoArgs 
   if (s < steps) step(s, af[0], af[1]);
   wait_loads<0>();   // no direct load may still be writing this workgroup's LDS
   lds_barrier();     // nobody reads the stages any more
-  finish<kKind>(a, b, tm * 128 + t.wm * 32, tn * 128 + t.wn * 64, tm != tn, lds + t.wave * (2 * 2048), acc, old);
+  finish<kKind>(a, b, tm * 128 + t.wm * 32, tn * 128 + t.wn * 64, tm != tn, lds + t.wave * (2 * 2048), acc, old, kept);
 }
 
 // The same with a 256 x 256 tile and the two-group loop of nt_tile.hpp. 8192 x 8192: the symmetric products 402 and 412 us and 14
@@ -510,12 +579,15 @@ __global__ __launch_bounds__(kNtThreads) void ortho_product128_kernel(OrthoArgs 
 template <int kKind>
 __global__ __launch_bounds__(kNtThreads) void ortho_product256_kernel(OrthoArgs a, Tiles tiles, Deal deal, float* __restrict__ work) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * kNtStage];
+  __shared__ __attribute__((aligned(16))) float diagonals[8][Kept::size(128)];
   const Share share = share_of(deal, static_cast<int>(blockIdx.x));
   const int b = share.tile / tiles.count;
   int tm, tn;
   tile_of(tiles, share.tile - b * tiles.count, tm, tn);
   NtTile t;
   t.init(lds, a.lda * 2, a.ldb * 2);
+  Kept kept;
+  kept.fetch<kKind, 128>(a, b, tm * 256 + t.wm * 128, tn * 256 + t.wn * 64, diagonals[t.wave]);
   const int steps = share.s1 - share.s0;
   NtOperand oa, ob;
   {
@@ -616,7 +688,8 @@ __global__ __launch_bounds__(kNtThreads) void ortho_product256_kernel(OrthoArgs 
       two[0][j] = acc[i][j];
       two[1][j] = acc[i + 1][j];
     }
-    finish<kKind, 2>(a, b, m, n0, tm != tn, lds + t.wave * (2 * 2048), two, old);
+    finish<kKind, 2>(a, b, m, n0, tm != tn, lds + t.wave * (2 * 2048), two, old, kept);
+    kept.rows += 32;
     tile_fence();
     m = next;
     __builtin_amdgcn_sched_barrier(0);
@@ -627,6 +700,7 @@ __global__ __launch_bounds__(kNtThreads) void ortho_product256_kernel(OrthoArgs 
 template <int kKind>
 __global__ __launch_bounds__(kNtThreads) void ortho_join_kernel(OrthoArgs a, Tiles tiles, Deal deal, float* __restrict__ work) {
   __shared__ __attribute__((aligned(1024))) char lds[8 * 4096];
+  __shared__ __attribute__((aligned(16))) float diagonals[8][Kept::size(16)];
   const int tile = deal.whole + static_cast<int>(blockIdx.x) / 8, i = static_cast<int>(blockIdx.x) & 7;
   const int b = tile / tiles.count;
   int tm, tn;
@@ -637,8 +711,11 @@ __global__ __launch_bounds__(kNtThreads) void ortho_join_kernel(OrthoArgs a, Til
   const int m0 = tm * 256 + (wave >> 2) * 128 + i * 16, n0 = tn * 256 + (wave & 3) * 64;
   Old<kKind, 1> old;
   old.fetch(a, b, m0, n0);
+  Kept kept;
+  kept.fetch<kKind, 16>(a, b, m0, n0, diagonals[wave]);
   join_parts(deal, work, tile, i, wave, lane, acc);
-  finish<kKind>(a, b, m0, n0, tm != tn, lds + wave * 4096, acc, old);
+  wait_loads<0>();   // the diagonals, which only this wave reads
+  finish<kKind>(a, b, m0, n0, tm != tn, lds + wave * 4096, acc, old, kept);
 }
 
 // ---- matrices with a short side --------------------------------------------------------------------
@@ -1188,7 +1265,7 @@ struct OrthoPlan {
   int64_t r, c, ldr, ldc;                    // W: r x ldc, U: c x ldr (fp16)
   bool small;
   int chunks;
-  int64_t u0, u1, lo, w, p, q, norms, scalars, parts, bytes;   // small: p and q are the shares of P
+  int64_t u0, u1, lo, w, p, q, dp, dq, norms, scalars, parts, bytes;   // small: p and q are the shares of P
 };
 OrthoPlan make_plan(int64_t batch, int64_t rows, int64_t cols) {
   OrthoPlan o{};
@@ -1219,6 +1296,8 @@ OrthoPlan make_plan(int64_t batch, int64_t rows, int64_t cols) {
     o.w = take(batch * o.r * o.ldc * 2);
     o.p = take(batch * o.r * o.ldr * 2);
     o.q = take(batch * o.r * o.ldr * 2);
+    o.dp = take(batch * o.ldr * 4);
+    o.dq = take(batch * o.ldr * 4);
     const int r = static_cast<int>(o.r), c = static_cast<int>(o.c);
     int64_t floats = part_floats(kGram, r, r, static_cast<int>(o.ldc), batch);
     for (const int64_t f : {part_floats(kSquare, r, r, static_cast<int>(o.ldr), batch), part_floats(kUpdate, c, r, static_cast<int>(o.ldr), batch)})
@@ -1268,6 +1347,7 @@ hipError_t launch_ortho(const OrthoLaunch& l, hipStream_t s) {
   const int64_t pieces = l.ld == l.cols || l.rows == 1 ? (l.rows * l.cols + kNormSpan - 1) / kNormSpan : l.rows * ((l.cols + kNormSpan - 1) / kNormSpan);
   const int parts = norm_parts(l.batch, pieces);
   float* part_work = reinterpret_cast<float*>(base + o.parts);
+  float *dp = reinterpret_cast<float*>(base + o.dp), *dq = reinterpret_cast<float*>(base + o.dq);
   if (o.small) {
     SmallArgs a{};
     a.norms = norms;
@@ -1314,6 +1394,7 @@ hipError_t launch_ortho(const OrthoLaunch& l, hipStream_t s) {
     g.K = static_cast<int>(o.ldc);
     g.scalars = i == 0 ? scalars : nullptr;
     g.f1 = kP / (kx * kx);
+    g.d_out = dp;
     g.D = g.T = p; g.ldc = g.ldt = o.ldr; g.batch_c = g.batch_t = bp;
     if ((e = product<kGram>(g, static_cast<int>(l.batch), part_work, s)) != hipSuccess) break;
     OrthoArgs h{};
@@ -1322,6 +1403,8 @@ hipError_t launch_ortho(const OrthoLaunch& l, hipStream_t s) {
     h.K = static_cast<int>(o.ldr);
     h.f1 = kq * l.b / kP;
     h.f2 = kq * l.c / (kP * kP);
+    h.d_in = dp;
+    h.d_out = dq;
     h.C = p; h.D = h.T = q; h.ldc = h.ldt = o.ldr; h.batch_c = h.batch_t = bp;
     if ((e = product<kSquare>(h, static_cast<int>(l.batch), part_work, s)) != hipSuccess) break;
     OrthoArgs x{};
@@ -1332,6 +1415,7 @@ hipError_t launch_ortho(const OrthoLaunch& l, hipStream_t s) {
     x.scalars = i == 0 ? scalars : nullptr;
     x.f1 = l.a;
     x.f2 = 1 / kq;
+    x.d_in = dq;
     x.C = x.A; x.D = i & 1 ? u0 : u1; x.ldc = o.ldr; x.batch_c = bu;
     x.lo_in = i == 0 ? lo0 : i <= kept ? lo : nullptr;
     x.lo_out = i < kept ? lo : nullptr;
