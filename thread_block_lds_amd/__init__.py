@@ -161,10 +161,21 @@ def _check(status, where, allow_warning=False):
     return status
 
 
+_torch = None
+
+
+def _load():
+    """torch, imported on first use; kept, since an import statement costs a tenth of a microsecond each time."""
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _on(stream, index):
     """(address, side) of the stream that a call on GPU ``index`` runs on: the current one, or ``stream``; side is the latter
     as a torch stream where it is not the current one, else None."""
-    import torch
+    torch = _torch or _load()
     here = torch._C._cuda_getCurrentRawStream(index)
     if stream is None or int(stream) == here:
         return here, None
@@ -174,7 +185,7 @@ def _on(stream, index):
 def _launch(index, fn, *args):
     """fn(*args) with GPU ``index`` as the current one: a default stream's address is 0 on every GPU, and means the current
     one's."""
-    import torch
+    torch = _torch or _load()
     if torch._C._cuda_getDevice() == index:
         return fn(*args)
     with torch.cuda.device(index):
@@ -185,7 +196,7 @@ def _buffer(shape, dtype, device, side, output=True):
     """A new buffer for a call that runs on ``side`` (None: the current stream), from that stream's pool: the current
     one's hands out blocks that kernels waiting there still use. An output is recorded on the current stream, where the
     caller may use and drop it."""
-    import torch
+    torch = _torch or _load()
     if side is None:
         return torch.empty(shape, dtype=dtype, device=device)
     here = torch.cuda.current_stream(device)
@@ -455,7 +466,7 @@ def quantize_fp8(x, fmt=None, rows=1, transposed=False, stream=None):
     ``transposed`` a pair of them, x and its transpose, from one pass over x. The codes' rows are stored
     at a stride of a multiple of 128 bytes, with zeros past the last column. Autograd does not see the call: the result
     carries no gradient, whatever x asks for."""
-    import torch
+    torch = _torch or _load()
     if not _x_types:
         _types()
     shape = x.shape
@@ -561,7 +572,7 @@ def gemm_fp8(a, b, add=None, out=None, out_dtype=None, workspace=None, stream=No
     scales' layouts of A and B may differ. workspace: a uint8 tensor of at least gemm_fp8_workspace(M, N, K)
     bytes (default: a fresh one). Returns C. Autograd does not see the call: a layer's backward is made of such
     products itself (examples/train_fp8_muon.py)."""
-    import torch
+    torch = _torch or _load()
     x_types = _x_types or _types()[0]
     device, index = a.codes.device, a.codes.get_device()
     address, side = _on(stream, index) if index >= 0 else (0, None)
@@ -613,7 +624,7 @@ def newton_schulz(x, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
 
     out: optional contiguous output of x's shape; out_dtype: default x's dtype. workspace: a uint8 tensor of at least
     newton_schulz_workspace(batch, R, C) bytes (default: a fresh one). Returns the output, which carries no gradient."""
-    import torch
+    torch = _torch or _load()
     x_types, _ = _types()
     if x.dim() != 2 and x.dim() != 3:
         raise ValueError(f"expected a matrix or a batch of them, got shape {tuple(x.shape)}")
