@@ -327,7 +327,7 @@ __device__ __forceinline__ void mend_range(const Gemm8Args& a, int g0, int g1, i
 
 // 256 x 256 tiles with the two-group loop of nt_tile.hpp (16-bit outputs). The scales have four slots of their own in
 // LDS and are read with the operands. A compute half-period is 16 matrix instructions of 32 cycles; the
-// 4 multiply-adds (kRowB: 4 products too) that follow each run beside the next one. 8192^3: 411 to 440 us, 2.5 to 2.67 PFLOP/s,
+// 4 multiply-adds (kRowB: 4 products too) that follow each run beside the next one. 8192^3: 405 to 449 us, 2.45 to 2.71 PFLOP/s,
 // against 3.08 of a library product of whole matrices without group scales. Bound by the board's power: the loop without the
 // multiply-adds takes 376 us, and the matrix unit is busy for two thirds of the cycles of a lowered clock.
 constexpr int kScaleSlot = 2 * 256 * 4;
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(kNtThreads) void gemm8_join_kernel(Gemm8Args a, Til
 
 // 128 x 128 tiles with the loop of nt_tile.hpp's Nt128 (16-bit outputs). Scales come with the operands and are read a
 // step ahead; a product is added to its sum three instructions later (the last three of a step in the next one). A group takes
-// 0.5 us: 777 x 4100 x 6100 30 us, one round of 231 tiles; 24 x 10240 x 6144, split three ways, 15.6 and 3.9 for joining.
+// 0.5 us: 777 x 4100 x 6100 30 to 31 us, one round of 231 tiles; 24 x 10240 x 6144, split three ways, 16 and 4 for joining.
 constexpr int kScale128 = 2 * 128 * 4;
 
 template <int kFa, int kFb, bool kRowB>
@@ -697,7 +697,7 @@ __global__ __launch_bounds__(kNtThreads) void gemm8_tile128_kernel(Gemm8Args a, 
 
 // fp32 outputs (exact products: twice the matrix cycles, and the conversions): 128 x 128 tiles, four waves of 64 x 64, two
 // stages of LDS, so that two workgroups share a CU and one's loads and epilogue hide behind the other's products. Few tiles are
-// split along k (exact_deal). 10240 x 6144 x 2000 with an addition: 303 us, of which 14.75 a group (16 of them, 1.09 PFLOP/s), bound
+// split along k (exact_deal). 10240 x 6144 x 2000 with an addition: 298 to 313 us, of which 14.75 a group (16 of them, 1.09 PFLOP/s), bound
 // by issue: a conversion or two and as many multiplications and multiply-adds to a matrix instruction; 40 writing, 30 adding
 // (311 with the addition at the end instead of at the start). Starting half the workgroups late changed nothing.
 template <int kFa, int kFb, bool kRowB>

@@ -84,7 +84,7 @@ struct Quant8Launch {
   int64_t rows, cols, ld;   // ld in elements
   int block;                // 1 or 128
   uint8_t* codes;
-  int64_t ldc;              // bytes, a multiple of 128
+  int64_t ldc;              // bytes, a multiple of 16, at least cols rounded up to 128
   float* scale;
   uint8_t* codes_t;         // nullable: the transpose's codes and scales
   int64_t ldt;

@@ -7,13 +7,13 @@
 // for X'^T = a U + U Q (P and Q are symmetric); the update writes both.
 //
 // Arithmetic: operands are fp16, sums fp32. fp16 has bf16's cost and eight times its precision; with bf16
-// operands the result is 1.4 % off the exact one, with fp16 0.1-0.2 % (the output's own bf16 rounding is 0.17 %). The
+// operands the result is 1.4 % off the exact one, with fp16 0.03-0.1 % (a bf16 output's own rounding is 0.17 %). The
 // values are held at powers of two that keep them normal numbers: X at kx (rms near 1 after the
 // normalisation), P at kP = 2^14 (its entries are at most 4 where the iteration is of any use), Q at kq. x itself is
 // scaled by a power of two only, so 16-bit inputs enter exactly, and 1 / (|x| + eps) is applied to
-// the fp32 sums of the first P and update. The term a X multiplies what rounding adds to the small singular values by a
-// in every step that follows (485 in five), so in all but the last two it takes X to 22 bits: U's remainder is kept
-// beside it, in fp16 too.
+// the fp32 sums of the first P and update. Two roundings are kept. The term a X multiplies what rounding adds to the small
+// singular values by a in every step that follows (485 in five), so in all but the last two steps it takes X to 22 bits: U's
+// remainder is kept beside it, in fp16 too. And P's and Q's diagonals (see finish).
 #include <stdint.h>
 
 #include "nt_tile.hpp"
@@ -573,8 +573,8 @@ __global__ __launch_bounds__(kNtThreads) void ortho_product128_kernel(OrthoArgs 
   finish<kKind>(a, b, tm * 128 + t.wm * 32, tn * 128 + t.wn * 64, tm != tn, lds + t.wave * (2 * 2048), acc, old, kept);
 }
 
-// The same with a 256 x 256 tile and the two-group loop of nt_tile.hpp. 8192 x 8192: the symmetric products 402 and 412 us and 14
-// for joining split tiles, the update 809: 1.33 to 1.36 PFLOP/s; a library product of the same size reaches 1.48. Bound by the
+// The same with a 256 x 256 tile and the two-group loop of nt_tile.hpp. 8192 x 8192: the symmetric products 411 and 421 us and 14
+// for joining split tiles, the update 825, the last 770: 1.3 to 1.43 PFLOP/s; a library product of the same size reaches 1.48. Bound by the
 // matrix instructions at the clock that the board's power allows.
 template <int kKind>
 __global__ __launch_bounds__(kNtThreads) void ortho_product256_kernel(OrthoArgs a, Tiles tiles, Deal deal, float* __restrict__ work) {
