@@ -488,7 +488,8 @@ int64_t tbl_gemm_fp8_workspace(int64_t M, int64_t N, int64_t K);
  *                 3.4445, -4.7750, 2.0315 do): operands are held in fp16
  *   workspace     device memory of tbl_newton_schulz_workspace(batch, rows, cols) bytes, 256-byte aligned
  * The norm is summed in 64 bits, products of fp16 operands in fp32: the result is 3e-4 to 1e-3 of its norm off, whatever
- * the types, and out_type's rounding. A matrix whose norm is not finite, or 0 with eps 0, gives NaN.
+ * the types, and out_type's rounding; more where eps is 2^10 |x| and beyond, whose X has subnormal fp16 entries. A matrix
+ * whose norm is not finite, or 0 with eps 0, gives NaN.
  * Sizes 0 .. 2^20, batch <= 65535. Empty: nothing is enqueued.
  */
 int tbl_newton_schulz(const void* x, int64_t batch, int64_t rows, int64_t cols, int64_t ldx, int64_t batch_stride,

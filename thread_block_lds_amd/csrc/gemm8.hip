@@ -260,8 +260,8 @@ __device__ __forceinline__ void add_scaled_wide(f32x4_t& acc, const f32x4_t& p, 
 
 // The loops take the product of two scales first, one multiplication a row and group instead of one a result. Where a wave's sums
 // (groups g0, g0 + step, ... below g1, of the rows from m0 and columns from n0, which began at start(i, j)) are not all finite
-// and a group of theirs has scales beyond fp32 together, they are taken again from memory with add_scaled_wide. Sums that are
-// not finite for another reason, a NaN or an infinity in a row, cost the look at the scales.
+// and its rows' largest finite scale and its columns' are beyond fp32 together, they are taken again from memory with
+// add_scaled_wide. Sums that are not finite for another reason, a NaN or an infinity in a row, cost the look at the scales.
 template <int kFa, int kFb, bool kRowB, bool kExact, int TM, int TN, class Start>
 __device__ __forceinline__ void mend_range(const Gemm8Args& a, int g0, int g1, int step, int m0, int n0, f32x4_t (&acc)[TM][TN], Start start) {
   constexpr float inf = __builtin_huge_valf();
@@ -276,19 +276,25 @@ __device__ __forceinline__ void mend_range(const Gemm8Args& a, int g0, int g1, i
   const int r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
   auto scale_a = [&](int m, int g) { return a.sa[(min(m, a.M - 1) >> a.a_shift) * a.sa_row + g * a.sa_group]; };
   auto scale_b = [&](int n, int g) { return a.sb[(min(n, a.N - 1) >> a.b_shift) * a.sb_row + g * a.sb_group]; };
-  bool wide = false;
-#pragma unroll 1
+  // the largest finite scales of the wave's rows and columns, a row or two and a column a lane, over all of its groups
+  const int lane = threadIdx.x & 63;
+  float most_a = 0, most_b = 0;
+  auto take = [&](float& most, float s) {
+    s = __builtin_fabsf(s);
+    if (s < inf) most = __builtin_fmaxf(most, s);
+  };
+#pragma unroll 4
   for (int g = g0; g < g1; g += step) {
-    float most = 0;   // of this lane's rows' finite scales
-#pragma unroll 1
-    for (int i = 0; i < TM; ++i) {
-      const float s = __builtin_fabsf(scale_a(m0 + 16 * i + r, g));
-      if (s < inf) most = __builtin_fmaxf(most, s);
-    }
-#pragma unroll 1
-    for (int n = 0; n < (kRowB ? 4 * TN : 1); ++n) wide |= beyond(most, scale_b(n0 + (kRowB ? 16 * (n >> 2) + 4 * q + (n & 3) : 0), g));
+#pragma unroll
+    for (int m = 0; m < TM; m += 4) take(most_a, scale_a(m0 + 16 * m + (lane & (16 * TM - 1)), g));
+    take(most_b, scale_b(n0 + (lane & (16 * TN - 1)), g));
   }
-  if (__builtin_amdgcn_ballot_w64(wide) == 0) return;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    most_a = __builtin_fmaxf(most_a, __shfl_xor(most_a, d));
+    most_b = __builtin_fmaxf(most_b, __shfl_xor(most_b, d));
+  }
+  if (!beyond(most_a, most_b)) return;
   auto fetch = [&](const uint8_t* p, int64_t ld, int row, int rows, int g) -> Codes {   // this lane's two chunks of a row
     uint4 c[2];
 #pragma unroll
